@@ -9,6 +9,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -29,7 +30,7 @@ HIP_FLAGS = [
     "-I", os.path.join(ROOT, "include"),
     "-I", CSRC,
 ]
-SOURCES = ["ns_kernels.hip", "ns_peak.hip", "ns_noalloc.hip", "ns_api.cpp"]
+SOURCES = ["ns_kernels.hip", "ns_peak.hip", "ns_noalloc.hip", "ns_host.cpp", "ns_api.cpp"]
 
 
 def hipcc():
@@ -39,23 +40,26 @@ def hipcc():
     raise RuntimeError("hipcc not found")
 
 
+def compile_source(src, tmp, verbose=False):
+    obj = os.path.join(tmp, os.path.splitext(src)[0] + ".o")
+    lang = ["-x", "hip"] if src.endswith(".hip") else []
+    cmd = [hipcc()] + HIP_FLAGS + lang + ["-c", os.path.join(CSRC, src), "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout)
+        raise RuntimeError(f"hipcc failed on {src}")
+    if verbose:
+        sys.stdout.write(r.stdout)
+    return obj
+
+
 def build(verbose=False):
-    objs = []
     tmp = os.path.join(PKG, "_build")
     os.makedirs(tmp, exist_ok=True)
-    for src in SOURCES:
-        obj = os.path.join(tmp, os.path.splitext(src)[0] + ".o")
-        lang = ["-x", "hip"] if src.endswith(".hip") else []
-        cmd = [hipcc()] + HIP_FLAGS + lang + ["-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-        if r.returncode != 0:
-            sys.stderr.write(r.stdout)
-            raise RuntimeError(f"hipcc failed on {src}")
-        if verbose:
-            sys.stdout.write(r.stdout)
-        objs.append(obj)
+    with ThreadPoolExecutor(4) as pool:
+        objs = list(pool.map(lambda src: compile_source(src, tmp, verbose), SOURCES))
     out_tmp = LIB + ".tmp"
     cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", out_tmp] + objs
     if verbose:

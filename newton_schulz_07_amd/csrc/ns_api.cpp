@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/ns_hip.h"
+#include "ns_host.h"
 #include "ns_kernels.h"
 #include "ns_layout.h"
 #include "ns_plan.h"
@@ -26,30 +27,23 @@ namespace {
 using ns::GemmArgs;
 using ns::NormArgs;
 using ns::Plan;
+using ns::check_arch;
+using ns::check_dtype;
+using ns::check_hip;
+using ns::check_ptr;
+using ns::fail;
+using ns::g_poison;
+using ns::get_workspace;
 using ns::make_plan;
-
-thread_local std::string t_err;
-thread_local std::string t_cfg;
-
-int fail(int status, const std::string& msg) {
-  t_err = msg;
-  return status;
-}
+using ns::overlaps;
+using ns::t_cfg;
+using ns::t_err;
+using ns::t_untimed;
+using ns::timed_launch;
 
 size_t esize(int dtype) { return ns::elem_size(dtype); }
 
-int check_hip(hipError_t e, const char* what) {
-  if (e == hipSuccess) return NS_OK;
-  return fail(NS_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
-}
-
 // ---------------------------------------------------------------- checks
-
-int check_dtype(int dtype) {
-  if (dtype != NS_DTYPE_F32 && dtype != NS_DTYPE_BF16)
-    return fail(NS_ERR_DTYPE, "dtype must be 0 (fp32) or 1 (bf16), got " + std::to_string(dtype));
-  return NS_OK;
-}
 
 // any_dims: rows and cols need not be multiples of 8 (ns_orthogonalize pads
 // such shapes; the stage exports do not)
@@ -64,132 +58,6 @@ int check_shape(int64_t batch, int64_t rows, int64_t cols, bool any_dims = false
     return fail(NS_ERR_INVALID_ARG, "a slice must hold fewer than 2^29 elements (2 GiB of fp32)");
   if (batch > 65535) return fail(NS_ERR_INVALID_ARG, "batch must be <= 65535");
   return NS_OK;
-}
-
-int check_ptr(const void* p, const char* name) {
-  if (p == nullptr) return fail(NS_ERR_INVALID_ARG, std::string(name) + " is NULL");
-  if (reinterpret_cast<uintptr_t>(p) % 16 != 0)
-    return fail(NS_ERR_ALIGNMENT, std::string(name) + " is not 16-byte aligned");
-  return NS_OK;
-}
-
-std::mutex g_arch_mu;
-std::map<int, int> g_arch;  // device -> NS_OK or NS_ERR_ARCH
-
-int check_arch() {
-  int dev = 0;
-  if (int s = check_hip(hipGetDevice(&dev), "hipGetDevice")) return s;
-  std::lock_guard<std::mutex> lk(g_arch_mu);
-  auto it = g_arch.find(dev);
-  if (it == g_arch.end()) {
-    hipDeviceProp_t prop;
-    if (int s = check_hip(hipGetDeviceProperties(&prop, dev), "hipGetDeviceProperties")) return s;
-    const int ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? NS_OK : NS_ERR_ARCH;
-    it = g_arch.emplace(dev, ok).first;
-    if (ok != NS_OK) t_err = std::string("device is ") + prop.gcnArchName + ", this library is built for gfx950";
-  }
-  if (it->second != NS_OK) return fail(NS_ERR_ARCH, "current device is not gfx950");
-  return NS_OK;
-}
-
-// ------------------------------------------------------------- workspace
-
-struct Ws {
-  void* ptr = nullptr;
-  size_t bytes = 0;
-};
-std::mutex g_ws_mu;
-std::map<std::pair<int, void*>, Ws> g_ws;
-// Buffers replaced by a larger one.  Work queued earlier may still read
-// them, and another thread may hold the pointer between taking it and
-// enqueueing its launches, so they are freed only by ns_release_workspace.
-std::vector<std::pair<int, void*>> g_ws_retired;
-std::atomic<int64_t> g_ws_allocs{0};
-
-// The workspace of (current device, st), grown to at least `bytes`.  A warm
-// workspace is returned without any HIP call, so calls on a stream that has
-// seen a call of the same or a larger size enqueue only kernels and copies
-// (graph capture needs exactly that).
-int get_workspace(hipStream_t st, size_t bytes, char** out) {
-  int dev = 0;
-  if (int s = check_hip(hipGetDevice(&dev), "hipGetDevice")) return s;
-  std::lock_guard<std::mutex> lk(g_ws_mu);
-  Ws& w = g_ws[{dev, (void*)st}];
-  if (w.bytes < bytes) {
-    void* p = nullptr;
-    if (hipMalloc(&p, bytes) != hipSuccess || p == nullptr) {
-      (void)hipGetLastError();
-      return fail(NS_ERR_OOM, "workspace allocation of " + std::to_string(bytes) + " bytes failed");
-    }
-    ++g_ws_allocs;
-    if (w.ptr != nullptr) g_ws_retired.emplace_back(dev, w.ptr);
-    w.ptr = p;
-    w.bytes = bytes;
-  }
-  *out = static_cast<char*>(w.ptr);
-  return NS_OK;
-}
-
-// ---------------------------------------------------------------- timing
-
-struct TimingRec {
-  int kind;
-  hipEvent_t a, b;
-};
-std::mutex g_t_mu;
-int g_t_mask = 0;
-int g_t_every = 1, g_t_offset = 0;     // launch i of a kind is timed when i % every == offset
-int64_t g_t_count[NS_KIND_COUNT] = {};  // launches of each kind since the last reset
-std::vector<TimingRec> g_t_recs;
-std::vector<hipEvent_t> g_t_pool;
-
-hipEvent_t take_event() {
-  if (!g_t_pool.empty()) {
-    hipEvent_t e = g_t_pool.back();
-    g_t_pool.pop_back();
-    return e;
-  }
-  // Timing-only events: no system-scope fence when recorded.  With the
-  // default flags every record writes back and invalidates the caches, which
-  // costs the timed kernels time of their own and slows the kernel after
-  // them.  Their timestamps are only read after the stream has been
-  // synchronised (ns_timing_query).
-  hipEvent_t e = nullptr;
-  if (hipEventCreateWithFlags(&e, hipEventDisableSystemFence) != hipSuccess) return nullptr;
-  return e;
-}
-
-// Set while the allocation-free entry point enqueues: its launches are
-// neither timed nor counted (timing may create events).
-thread_local bool t_untimed = false;
-
-// The events travel in the kernel's dispatch packet (ns::set_launch_events),
-// so timing adds no packets between the kernels of a call.
-template <typename F>
-hipError_t timed_launch(int kind, hipStream_t st, F&& f) {
-  if (t_untimed) return f();
-  std::unique_lock<std::mutex> lk(g_t_mu);
-  const bool on = ((g_t_mask >> kind) & 1) && g_t_count[kind]++ % g_t_every == g_t_offset;
-  hipEvent_t a = nullptr, b = nullptr;
-  if (on) {
-    a = take_event();
-    b = take_event();
-  }
-  lk.unlock();
-  const bool timed = on && a && b;
-  if (timed) ns::set_launch_events(a, b);
-  hipError_t e = f();
-  if (on) {
-    ns::set_launch_events(nullptr, nullptr);
-    lk.lock();
-    if (timed && e == hipSuccess) {
-      g_t_recs.push_back(TimingRec{kind, a, b});
-    } else {  // nothing recorded them: back to the pool
-      if (a) g_t_pool.push_back(a);
-      if (b) g_t_pool.push_back(b);
-    }
-  }
-  return e;
 }
 
 // ---------------------------------------------------------------- stages
@@ -268,12 +136,6 @@ int common_checks(int64_t batch, int64_t rows, int64_t cols, int dtype, bool any
   return check_shape(batch, rows, cols, any_dims);
 }
 
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const char* pa = static_cast<const char*>(a);
-  const char* pb = static_cast<const char*>(b);
-  return pa < pb + nb && pb < pa + na;
-}
-
 // ------------------------------------------------------- grouped calls
 
 // One stack of a grouped call: its plan, its part of the shared workspace
@@ -346,7 +208,6 @@ int check_grouped(int n, const void* const* in, void* const* out, const int64_t*
 // odd step count starts from a copy of the input.  With no step each stack
 // is normalised on its own (sum of squares, then scale).  *tc and launches
 // (Gram, poly, update launches of one step) describe what ran.
-std::atomic<int> g_poison{0};  // ns_set_workspace_poison
 
 //
 // The workspace is the library's cache for (device, st), or `given` (at
@@ -595,106 +456,6 @@ size_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, int dtype) 
   return make_plan(batch, rows, cols, dtype).total;
 }
 
-int ns_release_workspace(void) {
-  t_err.clear();
-  std::lock_guard<std::mutex> lk(g_ws_mu);
-  int status = NS_OK;
-  int cur = 0;
-  (void)hipGetDevice(&cur);
-  std::vector<std::pair<int, void*>> bufs = g_ws_retired;
-  for (auto& kv : g_ws)
-    if (kv.second.ptr != nullptr) bufs.emplace_back(kv.first.first, kv.second.ptr);
-  std::map<int, bool> synced;
-  for (auto& db : bufs) {
-    if (hipSetDevice(db.first) != hipSuccess) {
-      status = fail(NS_ERR_HIP, "hipSetDevice failed");
-      continue;
-    }
-    if (!synced[db.first]) {
-      (void)hipDeviceSynchronize();
-      synced[db.first] = true;
-    }
-    if (hipFree(db.second) != hipSuccess) status = fail(NS_ERR_HIP, "hipFree failed");
-  }
-  g_ws.clear();
-  g_ws_retired.clear();
-  (void)hipSetDevice(cur);
-  return status;
-}
-
-int64_t ns_workspace_allocations(void) { return g_ws_allocs.load(); }
-
-const char* ns_status_string(int status) {
-  switch (status) {
-    case NS_OK: return "NS_OK";
-    case NS_ERR_INVALID_ARG: return "NS_ERR_INVALID_ARG: invalid argument";
-    case NS_ERR_DTYPE: return "NS_ERR_DTYPE: unsupported dtype";
-    case NS_ERR_ALIGNMENT: return "NS_ERR_ALIGNMENT: pointers must be 16-byte aligned (stage exports: dims multiples of 8)";
-    case NS_ERR_ARCH: return "NS_ERR_ARCH: device is not gfx950";
-    case NS_ERR_OOM: return "NS_ERR_OOM: workspace allocation failed";
-    case NS_ERR_HIP: return "NS_ERR_HIP: HIP runtime error";
-    case NS_ERR_SCRATCH: return "NS_ERR_SCRATCH: the call needs more than the fixed no-alloc scratch";
-    default: return "unknown status";
-  }
-}
-
-const char* ns_last_error(void) { return t_err.c_str(); }
-
-int ns_query_last_config(char* buf, size_t n) {
-  if (buf != nullptr && n > 0) {
-    std::strncpy(buf, t_cfg.c_str(), n - 1);
-    buf[n - 1] = '\0';
-  }
-  return (int)t_cfg.size();
-}
-
-int ns_timing_enable(int mask) {
-  std::lock_guard<std::mutex> lk(g_t_mu);
-  g_t_mask = mask;
-  return NS_OK;
-}
-
-int ns_timing_sample(int every, int offset) {
-  t_err.clear();
-  if (every < 1 || offset < 0 || offset >= every)
-    return fail(NS_ERR_INVALID_ARG, "timing sample needs every >= 1 and 0 <= offset < every");
-  std::lock_guard<std::mutex> lk(g_t_mu);
-  g_t_every = every;
-  g_t_offset = offset;
-  return NS_OK;
-}
-
-int ns_timing_reset(void) {
-  std::lock_guard<std::mutex> lk(g_t_mu);
-  for (auto& c : g_t_count) c = 0;
-  for (auto& r : g_t_recs) {
-    g_t_pool.push_back(r.a);
-    g_t_pool.push_back(r.b);
-  }
-  g_t_recs.clear();
-  return NS_OK;
-}
-
-int ns_timing_query(int kind, double* total_ms, int64_t* launches) {
-  t_err.clear();
-  if (kind < 0 || kind >= NS_KIND_COUNT || total_ms == nullptr || launches == nullptr)
-    return fail(NS_ERR_INVALID_ARG, "bad timing query");
-  std::lock_guard<std::mutex> lk(g_t_mu);
-  double sum = 0.0;
-  int64_t count = 0;
-  for (auto& r : g_t_recs) {
-    if (r.kind != kind) continue;
-    if (hipEventSynchronize(r.b) != hipSuccess) return fail(NS_ERR_HIP, "hipEventSynchronize failed");
-    float ms = 0.0f;
-    if (hipEventElapsedTime(&ms, r.a, r.b) != hipSuccess) return fail(NS_ERR_HIP, "hipEventElapsedTime failed");
-    sum += ms;
-    ++count;
-  }
-  *total_ms = sum;
-  *launches = count;
-  return NS_OK;
-}
-
 int ns_stage_normalize(const void* x, void* x0, float* norms, int64_t batch, int64_t rows, int64_t cols,
                        int dtype, void* stream) {
   t_err.clear();
@@ -755,11 +516,6 @@ int ns_stage_update(const void* x, const void* c_off, const float* c_diag, void*
   if (int s = check_arch()) return s;
   const Plan p = make_plan(batch, rows, cols, dtype);
   return run_update(x, c_off, c_diag, x_out, p, static_cast<hipStream_t>(stream));
-}
-
-int ns_set_workspace_poison(int on) {
-  g_poison.store(on != 0);
-  return NS_OK;
 }
 
 int ns_peak_mfma(int dtype, int64_t iters, double* tflops, double* clock_mhz, void* stream) {
