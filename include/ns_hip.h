@@ -234,7 +234,11 @@ enum {
   NS_KIND_GRAM = 2,    /* lower-triangle X Xᵀ (mirrored or lower-only)    */
   NS_KIND_POLY = 3,    /* lower-triangle C = aI + bA + cAA with mirror     */
   NS_KIND_UPDATE = 4,  /* X' = C X (or X C for tall), diagonal folded     */
-  NS_KIND_COUNT = 5
+  NS_KIND_LAYER_NORM = 5,  /* layer norm, forward and backward            */
+  NS_KIND_ROUTE = 6,       /* routing with its plan, forward and backward */
+  NS_KIND_EXPERTS = 7,     /* the experts' products and their gradients   */
+  NS_KIND_COMBINE = 8,     /* weighted sum per token, and its gradient    */
+  NS_KIND_COUNT = 9
 };
 int ns_timing_enable(int mask);
 int ns_timing_sample(int every, int offset);
@@ -298,6 +302,157 @@ int ns_stage_poly(const void* a_off, const float* a_diag, void* c_off,
 int ns_stage_update(const void* x, const void* c_off, const float* c_diag,
                     void* x_out, int64_t batch, int64_t rows, int64_t cols,
                     int dtype, void* stream);
+
+/* ---- the mixture-of-experts sublayer ------------------------------------ */
+/*
+ * What stands around the expert stacks whose gradients ns_orthogonalize
+ * takes: layer norm, routing of tokens to experts, the experts' products with
+ * their gradients (the weight gradient is a stack [experts, fan_out, fan_in])
+ * and the weighted sum of the experts' outputs per token.
+ *
+ * The conventions above hold, with these additions:
+ *   - Matrices of tokens are row-major; where a leading dimension (ld...) is
+ *     given, rows are that many elements apart.  Every other operand is
+ *     contiguous.  Index, offset and fp32 vectors need 4-byte alignment only.
+ *   - Outputs share no memory with inputs or with each other
+ *     (NS_ERR_INVALID_ARG).
+ *   - A dimension of a row is at most 2^20, a row count below 2^31.
+ *   - Sums are taken in fp32 and every result is rounded once to its type.
+ *     No atomics touch a floating-point value: the same inputs give the same
+ *     bits.
+ *   - Index data on the device (ids, offsets, rows, slots) is not trusted:
+ *     values out of range are skipped, as said at each entry point, and never
+ *     lead outside a buffer.
+ */
+
+/*
+ * ns_layer_norm - y = (x - mean) rstd weight + bias over the columns of each
+ * row, rstd = 1 / sqrt(var + eps), var the mean squared distance from mean.
+ *
+ *   x         [rows, cols] dtype, rows ldx >= cols elements apart.
+ *   weight, bias
+ *             [cols] param_dtype, or NULL (1 and 0).
+ *   y         [rows, cols] dtype.
+ *   mean, rstd
+ *             fp32 [rows], or NULL; the backward pass needs them.
+ *   rows == 0 enqueues nothing.
+ */
+int ns_layer_norm(const void* x, int64_t ldx, const void* weight, const void* bias,
+                  void* y, float* mean, float* rstd, int64_t rows, int64_t cols,
+                  int dtype, int param_dtype, float eps, void* stream);
+
+/*
+ * ns_layer_norm_backward - gradients of ns_layer_norm from dy [rows, cols]:
+ *   dx [rows, cols] dtype, dweight and dbias [cols] param_dtype; each may be
+ *   NULL.  weight is the forward pass's (NULL: 1), mean and rstd are what it
+ *   returned.  With rows == 0 dweight and dbias become zero.  Uses library
+ *   workspace (8 bytes per column and block, at most 256 MiB).
+ */
+int ns_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                           const void* weight, const float* mean, const float* rstd,
+                           void* dx, void* dweight, void* dbias, int64_t rows,
+                           int64_t cols, int dtype, int param_dtype, void* stream);
+
+enum {
+  NS_SCORE_SOFTMAX = 0, /* over all the token's logits */
+  NS_SCORE_SIGMOID = 1  /* of each logit               */
+};
+
+/*
+ * ns_route - chooses top_k of `experts` experts for each token.
+ *
+ *   logits    [tokens, experts] dtype, rows ld elements apart.
+ *   bias      fp32 [experts], or NULL.  It moves the choice, not the weights.
+ *   ids       int32 [tokens, top_k]: the experts with the largest keys, in
+ *             descending order, equal keys by index.  The key is score + bias,
+ *             or with no bias the logit itself.
+ *   groups, top_groups, group_best
+ *             the experts form `groups` groups of neighbours, ranked by the
+ *             sum of their group_best (1 or 2) largest score + bias (scores
+ *             with no bias); only experts of the best top_groups are chosen.
+ *             1, 1 for no groups.
+ *   weights   fp32 [tokens, top_k]: scale s / (sum of the chosen s + 1e-20)
+ *             if renormalize, else scale s; s is the expert's score.
+ *   offsets, rows, slots
+ *             the plan of the experts' products, or all NULL: the choices
+ *             sorted by expert, in token order within one.  Expert e has the
+ *             sorted rows offsets[e] .. offsets[e + 1] (int32 [experts + 1]);
+ *             sorted row i holds token rows[i] (int32 [tokens * top_k]);
+ *             choice j of token t is sorted row slots[t, j] (int32).
+ *
+ * experts <= 1024, top_k <= 64, groups <= 64 and a divisor of experts.
+ * Keys that pass through exp are compared in 64 bits.  A logit of -inf has
+ * score 0 and comes last; a row of nothing else has weights 0.  A NaN key
+ * counts as -inf, a NaN score makes the weights it enters NaN; ids are always
+ * top_k distinct experts.
+ */
+int ns_route(const void* logits, int64_t ld, const float* bias, int32_t* ids,
+             float* weights, int32_t* offsets, int32_t* rows, int32_t* slots,
+             int64_t tokens, int64_t experts, int64_t top_k, int64_t groups,
+             int64_t top_groups, int group_best, int score, int renormalize,
+             float scale, int dtype, void* stream);
+
+/*
+ * ns_route_backward - dlogits [tokens, experts] dtype from dweights fp32
+ * [tokens, top_k], for the choice ids (which has no gradient).  An id outside
+ * [0, experts) is left out.
+ */
+int ns_route_backward(const void* logits, int64_t ld, const int32_t* ids,
+                      const float* dweights, void* dlogits, int64_t tokens,
+                      int64_t experts, int64_t top_k, int score, int renormalize,
+                      float scale, int dtype, void* stream);
+
+/*
+ * ns_experts_product - y[i] = x[rows[i]] W_e^T for every sorted row i of every
+ * expert e (a linear layer per expert, rows gathered on the way).
+ *
+ *   x         [n_x, fan_in] dtype, rows ldx elements apart (a multiple of 8);
+ *             read through rows it must hold less than 2 GiB.
+ *   rows      int32 [n_rows], or NULL: sorted row i is row i of x.  A row
+ *             number outside [0, n_x) reads as zeros.
+ *   w         [experts, fan_out, fan_in] dtype.
+ *   offsets   int32 [experts + 1] on the device, ascending from 0 to n_rows;
+ *             values are clamped to [0, n_rows], and rows of y that no expert
+ *             has are not written.
+ *   y         [n_rows, fan_out] dtype.
+ * fan_out and fan_in are multiples of 8 (NS_ERR_ALIGNMENT).
+ */
+int ns_experts_product(const void* x, int64_t ldx, int64_t n_x, const int32_t* rows,
+                       const void* w, const int32_t* offsets, void* y, int64_t n_rows,
+                       int64_t experts, int64_t fan_out, int64_t fan_in, int dtype,
+                       void* stream);
+
+/* ns_experts_input_grad - dx[i] = dy[i] W_e for every sorted row: dy
+ * [n_rows, fan_out], dx [n_rows, fan_in].  ns_experts_combine without weights
+ * adds the rows of dx up to the gradient of x. */
+int ns_experts_input_grad(const void* dy, const void* w, const int32_t* offsets,
+                          void* dx, int64_t n_rows, int64_t experts, int64_t fan_out,
+                          int64_t fan_in, int dtype, void* stream);
+
+/* ns_experts_weight_grad - dw[e] = sum over e's sorted rows of
+ * dy[i]^T x[rows[i]]: [experts, fan_out, fan_in] dtype, all of it written
+ * (zero for an expert without rows).  x, ldx, n_x, rows as in the product. */
+int ns_experts_weight_grad(const void* dy, const void* x, int64_t ldx, int64_t n_x,
+                           const int32_t* rows, const int32_t* offsets, void* dw,
+                           int64_t n_rows, int64_t experts, int64_t fan_out,
+                           int64_t fan_in, int dtype, void* stream);
+
+/* ns_experts_combine - out[t] = sum over j of weights[t, j] y[slots[t, j]]:
+ * y [n_rows, cols], out [tokens, cols] dtype, weights fp32 [tokens, top_k] or
+ * NULL (1).  A slot outside [0, n_rows) adds nothing.  cols is a multiple of
+ * 8. */
+int ns_experts_combine(const void* y, const int32_t* slots, const float* weights,
+                       void* out, int64_t tokens, int64_t top_k, int64_t n_rows,
+                       int64_t cols, int dtype, void* stream);
+
+/* ns_experts_combine_backward - dy[slots[t, j]] = weights[t, j] dout[t] and
+ * dweights[t, j] = <dout[t], y[slots[t, j]]> (fp32; zero for a slot out of
+ * range); either may be NULL.  Rows of dy that no slot names are not
+ * written; no two choices may name the same row. */
+int ns_experts_combine_backward(const void* dout, const void* y, const int32_t* slots,
+                                const float* weights, void* dy, float* dweights,
+                                int64_t tokens, int64_t top_k, int64_t n_rows,
+                                int64_t cols, int dtype, void* stream);
 
 #ifdef __cplusplus
 }

@@ -18,6 +18,7 @@ NS_DTYPE_F32 = 0
 NS_DTYPE_BF16 = 1
 
 NS_KIND_SUMSQ, NS_KIND_SCALE, NS_KIND_GRAM, NS_KIND_POLY, NS_KIND_UPDATE = range(5)
+NS_KIND_LAYER_NORM, NS_KIND_ROUTE, NS_KIND_EXPERTS, NS_KIND_COMBINE = range(5, 9)
 KIND_NAMES = {NS_KIND_SUMSQ: "sumsq", NS_KIND_SCALE: "scale", NS_KIND_GRAM: "gram",
               NS_KIND_POLY: "poly", NS_KIND_UPDATE: "update"}
 
@@ -48,6 +49,16 @@ SIGNATURES = {
     "ns_stage_gram": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _int, _vp]),
     "ns_stage_poly": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _int, _flt, _flt, _flt, _vp]),
     "ns_stage_update": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp]),
+    "ns_layer_norm": (_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _flt, _vp]),
+    "ns_layer_norm_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _vp]),
+    "ns_route": (_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int, _int, _int, _flt,
+                        _int, _vp]),
+    "ns_route_backward": (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _flt, _int, _vp]),
+    "ns_experts_product": (_int, [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp]),
+    "ns_experts_input_grad": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp]),
+    "ns_experts_weight_grad": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp]),
+    "ns_experts_combine": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp]),
+    "ns_experts_combine_backward": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp]),
 }
 
 _lib = None
@@ -325,3 +336,25 @@ def ns_stage_update(x, c_off, c_diag):
         _check(lib().ns_stage_update(_ptr(x), _ptr(c_off), _ptr(c_diag), _ptr(x_out), batch, rows, cols,
                                      _dtype_code(x), _stream(x)))
     return x_out
+
+
+# ------------------------------------- the mixture-of-experts sublayer
+
+# The operators' binding needs torch, which the rest of this module loads only
+# when it is called: its names are looked up on first use.
+_SUBLAYER = ("Routing", "NS_SCORE_SOFTMAX", "NS_SCORE_SIGMOID", "ns_layer_norm", "ns_layer_norm_backward", "ns_route",
+             "ns_route_backward", "ns_experts_product", "ns_experts_input_grad", "ns_experts_weight_grad",
+             "ns_experts_combine", "ns_experts_combine_backward")
+
+
+def __getattr__(name):
+    if name in _SUBLAYER:
+        from . import sublayer
+        for n in _SUBLAYER:
+            globals()[n] = getattr(sublayer, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *_SUBLAYER})

@@ -30,7 +30,8 @@ HIP_FLAGS = [
     "-I", os.path.join(ROOT, "include"),
     "-I", CSRC,
 ]
-SOURCES = ["ns_kernels.hip", "ns_peak.hip", "ns_noalloc.hip", "ns_host.cpp", "ns_api.cpp"]
+SOURCES = ["ns_kernels.hip", "ns_peak.hip", "ns_noalloc.hip", "ns_norm.hip", "ns_route.hip", "ns_experts.hip",
+           "ns_host.cpp", "ns_api.cpp", "ns_sublayer.cpp"]
 
 
 def hipcc():

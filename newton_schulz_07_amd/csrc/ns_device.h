@@ -56,6 +56,32 @@ template <> struct Quad<float> {
   }
 };
 
+// 8 consecutive elements as they are stored
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16> { uint4 a; };
+template <> struct Raw8<float> { uint4 a, b; };
+
+__device__ __forceinline__ void unpack8(const Raw8<bf16>& r, float* f) {
+  f[0] = bf16_lo(r.a.x); f[1] = bf16_hi(r.a.x); f[2] = bf16_lo(r.a.y); f[3] = bf16_hi(r.a.y);
+  f[4] = bf16_lo(r.a.z); f[5] = bf16_hi(r.a.z); f[6] = bf16_lo(r.a.w); f[7] = bf16_hi(r.a.w);
+}
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float* f) {
+  f[0] = __uint_as_float(r.a.x); f[1] = __uint_as_float(r.a.y);
+  f[2] = __uint_as_float(r.a.z); f[3] = __uint_as_float(r.a.w);
+  f[4] = __uint_as_float(r.b.x); f[5] = __uint_as_float(r.b.y);
+  f[6] = __uint_as_float(r.b.z); f[7] = __uint_as_float(r.b.w);
+}
+__device__ __forceinline__ Raw8<bf16> pack8(const float* f, bf16) {
+  return Raw8<bf16>{make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                               pack_bf16(f[6], f[7]))};
+}
+__device__ __forceinline__ Raw8<float> pack8(const float* f, float) {
+  return Raw8<float>{make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                __float_as_uint(f[3])),
+                     make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                                __float_as_uint(f[7]))};
+}
+
 // 16-byte chunks of operand values -> one MFMA step of a 32x32 block.
 // bf16: the chunk is the 8-element k slice of v_mfma_f32_32x32x16_bf16.
 // fp32: the chunk is 4 k values, one per v_mfma_f32_32x32x2_f32; both
@@ -156,13 +182,17 @@ __device__ __forceinline__ int nat_lane_byte(int rb, int h, int lane, int rc, fl
 extern thread_local hipEvent_t t_ev_start, t_ev_stop;
 
 template <typename K, typename... A>
-static void dispatch(K kernel, dim3 grid, dim3 block, hipStream_t st, A... args) {
+static void dispatch_lds(K kernel, dim3 grid, dim3 block, size_t lds, hipStream_t st, A... args) {
   if (t_ev_start == nullptr && t_ev_stop == nullptr) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, st, args...);
+    hipLaunchKernelGGL(kernel, grid, block, lds, st, args...);
     return;
   }
-  hipExtLaunchKernelGGL(kernel, grid, block, 0, st, t_ev_start, t_ev_stop, 0, args...);
+  hipExtLaunchKernelGGL(kernel, grid, block, lds, st, t_ev_start, t_ev_stop, 0, args...);
   t_ev_start = nullptr;  // a later launch of the same kind moves only the stop
+}
+template <typename K, typename... A>
+static void dispatch(K kernel, dim3 grid, dim3 block, hipStream_t st, A... args) {
+  dispatch_lds(kernel, grid, block, 0, st, args...);
 }
 
 }  // namespace ns

@@ -1,0 +1,515 @@
+// ns_experts.hip - the products of a stack of experts with the rows routed
+// to them, their gradients, and the weighted sum of the results per token.
+//
+//   product          y[i]  = x[rows[i]] W_eᵀ              i in expert e's rows
+//   input gradient   dx[i] = dy[i] W_e
+//   weight gradient  dW_e  = sum_i dy[i]ᵀ x[rows[i]]
+//
+// One tiled MFMA kernel runs all three: acc(i, j) = sum_k P(i, k) Q(j, k)
+// with each operand read as K-contiguous rows or in its natural layout
+// (ns_layout.h), so neither x nor W is ever gathered or transposed in memory:
+//   product          P = rows of x, gathered   Q = rows of W_e
+//   input gradient   P = rows of dy            Q = columns of W_e (natural)
+//   weight gradient  P = columns of dy (natural), Q = columns of x (natural,
+//                    gathered): k runs over the expert's rows
+// Sums are in fp32 and rounded once.
+//
+// The experts' row counts are known on the device only.  The grid holds the
+// most tiles that n_rows rows can make; every workgroup adds up the experts'
+// tiles (one prefix sum by each wave) and takes its own, or ends.
+#include <type_traits>
+
+#include "ns_device.h"
+#include "ns_sublayer.h"
+
+namespace ns {
+namespace {
+
+constexpr unsigned kOutOfRange = 0x80000000u;  // past every descriptor below
+
+struct Tile {
+  int expert, tile;  // tile: row tile within the expert
+  int begin, count;  // the expert's sorted rows
+};
+
+// Row tiles of all experts, and the running count at the end of each lane's
+// experts (lane l: experts l per .. l per + per - 1).
+__device__ __forceinline__ void expert_rows(const int* offsets, int e, int experts, int n_rows, int* begin, int* count) {
+  *begin = *count = 0;
+  if ((unsigned)e >= (unsigned)experts) return;
+  const int b = min(max(offsets[e], 0), n_rows), c = min(max(offsets[e + 1], 0), n_rows);
+  *begin = b;
+  *count = c > b ? c - b : 0;
+}
+__device__ __forceinline__ int count_tiles(const ExpertsArgs& g, int bm, int* upto) {
+  const int lane = threadIdx.x & 63, per = (g.experts + 63) / 64;
+  int n = 0;
+  for (int i = 0; i < per; ++i) {
+    int b, c;
+    expert_rows(g.offsets, lane * per + i, g.experts, g.n_rows, &b, &c);
+    n += (c + bm - 1) / bm;
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(n, o, 64);
+    if (lane >= o) n += u;
+  }
+  *upto = n;
+  return __builtin_amdgcn_readlane(n, 63);
+}
+__device__ __forceinline__ Tile find_tile(const ExpertsArgs& g, int bm, int upto, int q) {
+  const int per = (g.experts + 63) / 64;
+  const int l = __ffsll((unsigned long long)__ballot(upto > q)) - 1;
+  int left = q - (l > 0 ? __builtin_amdgcn_readlane(upto, l - 1) : 0);
+  Tile t{};
+  for (int i = 0; i < per; ++i) {
+    int b, c;
+    expert_rows(g.offsets, l * per + i, g.experts, g.n_rows, &b, &c);
+    const int n = (c + bm - 1) / bm;
+    if (left < n) {
+      t = Tile{l * per + i, left, b, c};
+      break;
+    }
+    left -= n;
+  }
+  t.expert = __builtin_amdgcn_readfirstlane(t.expert);
+  t.tile = __builtin_amdgcn_readfirstlane(t.tile);
+  t.begin = __builtin_amdgcn_readfirstlane(t.begin);
+  t.count = __builtin_amdgcn_readfirstlane(t.count);
+  return t;
+}
+
+typedef const __attribute__((address_space(4))) int* ConstInts;  // read with scalar loads
+
+template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, int MODE>
+__global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_kernel(const ExpertsArgs g) {
+  constexpr bool PNAT = MODE == EXP_WEIGHT_GRAD, QNAT = MODE != EXP_PRODUCT;
+  constexpr int NW = WM * WN, NT = NW * 64;
+  constexpr int EPC = Elem<T>::kChunk, ES = (int)sizeof(T), BK = CPR * EPC;
+  constexpr int WTM = BM / WM, WTN = BN / WN, SM = WTM / 32, SN = WTN / 32;
+  constexpr int LP = BM * CPR, LQ = BN * CPR, STAGE = LP + LQ;
+  constexpr int NIW = STAGE / 64 / NW;
+  constexpr int ERC = epi_row_chunks(BN, ES);
+  constexpr int RCP = BM / EPC, RCQ = BN / EPC;
+  static_assert(WTM % 32 == 0 && WTN % 32 == 0, "wave tile must be whole 32x32 blocks");
+  static_assert(STAGE % (64 * NW) == 0 && (LP / 64) % NIW == 0, "a wave loads one operand");
+  static_assert(ST >= 2 && NIW * (ST - 2) < 64, "ring depth");
+  __shared__ uint4 lds[lds_chunks(BM, BN, CPR, ST, ES)];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int M = MODE == EXP_WEIGHT_GRAD ? g.fan_out : 0;  // output rows (else the expert's)
+  const int N = MODE == EXP_PRODUCT ? g.fan_out : g.fan_in;
+  const int tiles_n = (N + BN - 1) / BN;
+
+  // this workgroup's tile
+  Tile tl;
+  int i0, j0;
+  if (MODE == EXP_WEIGHT_GRAD) {
+    const int tiles_m = (M + BM - 1) / BM, per = tiles_m * tiles_n;
+    const int lin = xcd_remap(blockIdx.x, gridDim.x);
+    const int e = lin / per;
+    int ti, tj;
+    rect_decode(lin - e * per, tiles_m, tiles_n, ti, tj);
+    tl.expert = e;
+    tl.tile = ti;
+    expert_rows(g.offsets, e, g.experts, g.n_rows, &tl.begin, &tl.count);
+    i0 = ti * BM;
+    j0 = tj * BN;
+  } else {
+    int upto;
+    const int total = count_tiles(g, BM, &upto) * tiles_n;
+    // each XCD takes a contiguous run of the live tiles (xcd_remap)
+    const int xcd = blockIdx.x % 8, local = blockIdx.x / 8, per = total / 8, rem = total % 8;
+    if (local >= per + (xcd < rem ? 1 : 0)) return;
+    const int lin = xcd * per + min(xcd, rem) + local;
+    tl = find_tile(g, BM, upto, lin / tiles_n);
+    if (tl.count <= 0) return;  // (only offsets that are no prefix sums lead here)
+    i0 = tl.tile * BM;
+    j0 = (lin % tiles_n) * BN;
+  }
+  const int K = MODE == EXP_PRODUCT ? g.fan_in : MODE == EXP_INPUT_GRAD ? g.fan_out : tl.count;
+  const int m_end = MODE == EXP_WEIGHT_GRAD ? M : tl.count;
+
+  // Sources.  A wave loads chunks of one operand only.
+  const bool is_p = wave * NIW * 64 < LP;
+  const T* base;       // descriptor base (weight gradient: moved at each stage)
+  size_t bytes;        // descriptor length
+  unsigned off[NIW];   // byte offset at k0 = 0, kOutOfRange for rows and columns past the end
+  unsigned step = BK * ES;
+  const T* W = reinterpret_cast<const T*>(g.w) + (size_t)tl.expert * g.fan_out * g.fan_in;
+  if constexpr (MODE == EXP_WEIGHT_GRAD) {
+    base = is_p ? reinterpret_cast<const T*>(g.dy) + (size_t)tl.begin * g.fan_out
+                : reinterpret_cast<const T*>(g.x) + (g.rows ? 0 : (size_t)tl.begin * g.ldx);
+    bytes = 0;
+  } else if (is_p) {
+    const long long ld = MODE == EXP_PRODUCT ? g.ldx : g.fan_out;
+    const bool gather = MODE == EXP_PRODUCT && g.rows != nullptr;
+    base = reinterpret_cast<const T*>(MODE == EXP_PRODUCT ? g.x : g.dy) + (gather ? 0 : (tl.begin + i0) * ld);
+    bytes = gather ? ((size_t)(g.n_x - 1) * ld + g.fan_in) * ES
+                   : ((size_t)(min(BM, tl.count - i0) - 1) * ld + K) * ES;
+#pragma unroll
+    for (int t = 0; t < NIW; ++t) {
+      const DmaSrc d = dma_src(wave * NIW + t, lane, BM, BN, CPR, EPC, false, QNAT, ES);
+      int r = d.row;
+      bool ok = i0 + r < tl.count;
+      if (gather) {
+        r = ok ? g.rows[tl.begin + i0 + r] : 0;
+        ok = ok && (unsigned)r < (unsigned)g.n_x;
+      } else if (MODE == EXP_PRODUCT) {
+        ok = ok && tl.begin + i0 + r < g.n_x;
+      }
+      off[t] = ok ? (unsigned)(((size_t)r * ld + d.kpos) * ES) : kOutOfRange;
+    }
+  } else {
+    base = W;
+    bytes = (size_t)g.fan_out * g.fan_in * ES;
+    if (QNAT) step = (unsigned)(BK * g.fan_in * ES);
+#pragma unroll
+    for (int t = 0; t < NIW; ++t) {
+      const DmaSrc d = dma_src(wave * NIW + t, lane, BM, BN, CPR, EPC, false, QNAT, ES);
+      const int j = j0 + d.row;
+      off[t] = j >= N ? kOutOfRange
+                      : (unsigned)((QNAT ? (size_t)d.kpos * g.fan_in + j : (size_t)j * g.fan_in + d.kpos) * ES);
+    }
+  }
+  // weight gradient: this wave's k rows of a stage are kr0 .. kr0 + KR - 1,
+  // RPI to an instruction; x's row numbers are read one stage ahead
+  constexpr int RC = BM / EPC, RPI = 64 / RC, KR = NIW * RPI;
+  static_assert(MODE != EXP_WEIGHT_GRAD || (BM == BN && KR <= 16), "square tiles");
+  const int kr0 = MODE == EXP_WEIGHT_GRAD ? (wave * NIW * 64 - (is_p ? 0 : LP)) / RC : 0;
+  int idx[MODE == EXP_WEIGHT_GRAD ? KR : 1];
+  const ConstInts rows_c = (ConstInts)(unsigned long long)(g.rows + (g.rows ? tl.begin : 0));
+  auto read_idx = [&](int kt) __attribute__((always_inline)) {
+    if constexpr (MODE == EXP_WEIGHT_GRAD) {
+      if (is_p || g.rows == nullptr || kt * BK + kr0 >= K) return;
+      const int k = kt * BK + kr0;
+      if (k + KR <= K) {
+#pragma unroll
+        for (int r = 0; r < KR; ++r) idx[r] = rows_c[k + r];
+      } else {
+#pragma unroll
+        for (int r = 0; r < KR; ++r) idx[r] = rows_c[min(k + r, K - 1)];
+      }
+    }
+  };
+
+  auto issue = [&](int kt, int slot) __attribute__((always_inline)) {
+    const int k0 = kt * BK;
+    if constexpr (MODE == EXP_WEIGHT_GRAD) {
+      const long long ld = is_p ? (long long)g.fan_out : g.ldx;
+      const bool gather = !is_p && g.rows != nullptr;
+      const int left = K - k0;  // > 0
+      const i32x4 rs = make_rsrc(base + (gather ? 0 : k0 * ld),
+                                 gather ? (unsigned)(((size_t)(g.n_x - 1) * ld + g.fan_in) * ES)
+                                        : (unsigned)(((size_t)(min(BK, left) - 1) * ld + (is_p ? g.fan_out : g.fan_in)) * ES));
+#pragma unroll
+      for (int t = 0; t < NIW; ++t) {
+        const DmaSrc d = dma_src(wave * NIW + t, lane, BM, BN, CPR, EPC, true, true, ES);
+        const int c = (is_p ? i0 : j0) + d.row;
+        int r = d.kpos;
+        bool ok = c < (is_p ? M : N) && d.kpos < left;
+        if (!is_p) {
+          if (gather) {
+            r = idx[t * RPI];
+#pragma unroll
+            for (int u = 1; u < RPI; ++u)
+              if (lane / RC == u) r = idx[t * RPI + u];
+            ok = ok && (unsigned)r < (unsigned)g.n_x;
+          } else {
+            ok = ok && tl.begin + k0 + r < g.n_x;
+          }
+        }
+        dma16(lds_addr(lds + slot * STAGE + (wave * NIW + t) * 64),
+              ok ? (unsigned)(r * (unsigned)(ld * ES) + (unsigned)(c * ES)) : kOutOfRange, rs);
+      }
+      read_idx(kt + 1);
+    } else {
+      const i32x4 rs = make_rsrc(base, (unsigned)bytes);
+      const bool whole = k0 + BK <= K;
+#pragma unroll
+      for (int t = 0; t < NIW; ++t) {
+        const int kpos = dma_src(wave * NIW + t, lane, BM, BN, CPR, EPC, false, QNAT, ES).kpos;
+        // (an offset out of range stays there: step * kt is below 2^31)
+        dma16(lds_addr(lds + slot * STAGE + (wave * NIW + t) * 64),
+              whole || k0 + kpos < K ? off[t] + (unsigned)kt * step : kOutOfRange, rs);
+      }
+    }
+  };
+
+  f32x16 acc[SM][SN];
+#pragma unroll
+  for (int a = 0; a < SM; ++a)
+#pragma unroll
+    for (int b = 0; b < SN; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
+
+  // fragment reads: a per-lane base plus a compile-time offset
+  constexpr int KS = CPR / 2, NH = sizeof(T) == 2 ? 2 : 4, QOFF = LP * 16;
+  constexpr int NSP = nat_step_bytes(RCP, ES), NSQ = nat_step_bytes(RCQ, ES);
+  int kcp[PNAT ? 1 : KS], kcq[QNAT ? 1 : KS];
+  int natp[PNAT ? SM : 1][NH], natq[QNAT ? SN : 1][NH];
+  if constexpr (PNAT) {
+#pragma unroll
+    for (int a = 0; a < SM; ++a)
+#pragma unroll
+      for (int h = 0; h < NH; ++h) natp[a][h] = nat_lane_byte(wm * WTM + 32 * a, h, lane, RCP, T());
+  } else {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) kcp[s] = kc_lane_byte(wm * WTM, s, lane, CPR);
+  }
+  if constexpr (QNAT) {
+#pragma unroll
+    for (int b = 0; b < SN; ++b)
+#pragma unroll
+      for (int h = 0; h < NH; ++h) natq[b][h] = nat_lane_byte(wn * WTN + 32 * b, h, lane, RCQ, T()) + QOFF;
+  } else {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) kcq[s] = kc_lane_byte(wn * WTN, s, lane, CPR) + QOFF;
+  }
+  const char* lb = reinterpret_cast<const char*>(lds);
+  auto load_step = [&](int slot, int s, uint4 (&pf)[SM], uint4 (&qf)[SN]) __attribute__((always_inline)) {
+    const char* st = lb + slot * STAGE * 16;
+#pragma unroll
+    for (int a = 0; a < SM; ++a) {
+      if constexpr (PNAT) pf[a] = nat_frag(st + s * NSP, natp[a], T());
+      else pf[a] = *reinterpret_cast<const uint4*>(st + kcp[s ^ kc_sigma(a, CPR)] + a * 32 * CPR * 16);
+    }
+#pragma unroll
+    for (int b = 0; b < SN; ++b) {
+      if constexpr (QNAT) qf[b] = nat_frag(st + s * NSQ, natq[b], T());
+      else qf[b] = *reinterpret_cast<const uint4*>(st + kcq[s ^ kc_sigma(b, CPR)] + b * 32 * CPR * 16);
+    }
+  };
+  auto compute = [&](int slot) __attribute__((always_inline)) {
+    uint4 pf[2][SM], qf[2][SN];
+    load_step(slot, 0, pf[0], qf[0]);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      if (s + 1 < KS) load_step(slot, s + 1, pf[(s + 1) & 1], qf[(s + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);  // keeps these reads ahead of the MFMAs
+#pragma unroll
+      for (int a = 0; a < SM; ++a)
+#pragma unroll
+        for (int b = 0; b < SN; ++b) mfma_chunk(acc[a][b], qf[s & 1][b], pf[s & 1][a], T());
+    }
+  };
+
+  // Ring of ST stages: stage kt lives in slot kt % ST; before computing it a
+  // wave waits for its own loads of it, and the barrier publishes every
+  // wave's and certifies that slot (kt - 1) % ST is no longer read.
+  const int nk = (K + BK - 1) / BK;
+  auto stage = [&](int kt, int u) __attribute__((always_inline)) {
+    const int after = nk - 1 - kt;
+    if (after >= ST - 2) wait_vm_lgkm0<NIW * (ST - 2)>();
+    else wait_vm_lgkm0<0>();
+    ring_barrier();
+    if (kt + ST - 1 < nk) issue(kt + ST - 1, (u + ST - 1) % ST);
+    compute(u);
+  };
+  static_assert(ST <= 3, "the tail wait assumes at most one later stage in flight");
+  read_idx(0);
+#pragma unroll
+  for (int s = 0; s < ST - 1; ++s)
+    if (s < nk) issue(s, s);
+  int kt0 = 0;
+  for (; kt0 + ST <= nk; kt0 += ST) {
+#pragma unroll
+    for (int u = 0; u < ST; ++u) stage(kt0 + u, u);
+  }
+#pragma unroll
+  for (int u = 0; u < ST - 1; ++u)
+    if (kt0 + u < nk) stage(kt0 + u, u);
+  wait_vm_lgkm0<0>();
+  __syncthreads();
+
+  // the tile through LDS to whole 16-byte stores
+  T* O = reinterpret_cast<T*>(g.out) +
+         (MODE == EXP_WEIGHT_GRAD ? (size_t)tl.expert * g.fan_out * g.fan_in : (size_t)tl.begin * N);
+  T* S = reinterpret_cast<T*>(lds);
+  constexpr int SROW = ERC * EPC;
+#pragma unroll
+  for (int a = 0; a < SM; ++a)
+#pragma unroll
+    for (int b = 0; b < SN; ++b)
+#pragma unroll
+      for (int rg = 0; rg < 4; ++rg) {
+        const float v[4] = {acc[a][b][4 * rg], acc[a][b][4 * rg + 1], acc[a][b][4 * rg + 2], acc[a][b][4 * rg + 3]};
+        *reinterpret_cast<typename Quad<T>::Raw*>(S + (wm * WTM + a * 32 + acc_i(lane)) * SROW + wn * WTN + b * 32 +
+                                                  acc_j(rg, lane)) = Quad<T>::pack(v);
+      }
+  __syncthreads();
+  constexpr int CPT = BN / EPC;
+  for (int qd = tid; qd < BM * CPT; qd += NT) {
+    const int il = qd / CPT, c = qd % CPT;
+    const int i = i0 + il, j = j0 + c * EPC;
+    if (i >= m_end || j >= N) continue;
+    *reinterpret_cast<uint4*>(O + (size_t)i * N + j) = *reinterpret_cast<const uint4*>(S + il * SROW + c * EPC);
+  }
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, int MODE>
+hipError_t launch_tiles(const ExpertsArgs& g, hipStream_t st) {
+  const int N = MODE == EXP_PRODUCT ? g.fan_out : g.fan_in;
+  const long long tiles_n = (N + BN - 1) / BN;
+  long long grid;
+  if (MODE == EXP_WEIGHT_GRAD) {
+    grid = (long long)g.experts * ((g.fan_out + BM - 1) / BM) * tiles_n;
+  } else {
+    // sum of ceil(c / BM) over at most min(experts, n_rows) non-empty experts
+    const long long some = g.experts < g.n_rows ? g.experts : g.n_rows;
+    grid = ((g.n_rows + some * (BM - 1)) / BM) * tiles_n;
+    grid = (grid + 7) / 8 * 8;  // every XCD reaches its last live tile
+  }
+  if (grid <= 0) return hipSuccess;
+  if (grid > 0x7fffffffll) return hipErrorInvalidValue;
+  dispatch(experts_kernel<T, BM, BN, WM, WN, CPR, ST, OCC, MODE>, dim3((unsigned)grid), dim3(WM * WN * 64), st, g);
+  return hipGetLastError();
+}
+
+template <int MODE>
+hipError_t launch_mode(int dtype, const ExpertsArgs& g, hipStream_t st) {
+  if (dtype == 1) return launch_tiles<bf16, 128, 128, 2, 4, 8, 2, 2, MODE>(g, st);
+  return launch_tiles<float, 128, 128, 2, 2, 8, 3, 1, MODE>(g, st);
+}
+
+// ---------------------------------------------------------------- combine
+
+// out[t] = sum_j weights[t, j] y[slots[t, j]]: a thread to 8 columns of a
+// token; eight rows are on their way before the first is added.
+constexpr int kCombineAhead = 8;
+template <typename T>
+__global__ __launch_bounds__(256) void combine_kernel(const CombineArgs g) {
+  const int vpr = g.cols / 8;
+  long long t;
+  int v;
+  if (vpr >= 256) {
+    t = blockIdx.x;
+    v = blockIdx.y * 256 + threadIdx.x;
+  } else {
+    const int tpb = 256 / vpr, tl = threadIdx.x / vpr;
+    t = (long long)blockIdx.x * tpb + tl;
+    v = threadIdx.x - tl * vpr;
+    if (tl >= tpb) return;
+  }
+  if (t >= g.tokens || v >= vpr) return;
+  const Raw8<T>* y = reinterpret_cast<const Raw8<T>*>(g.y);
+  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int j0 = 0; j0 < g.top_k; j0 += kCombineAhead) {
+    Raw8<T> r[kCombineAhead];
+    float w[kCombineAhead];
+#pragma unroll
+    for (int u = 0; u < kCombineAhead; ++u) {
+      r[u] = Raw8<T>{};
+      w[u] = 0.0f;
+      if (j0 + u >= g.top_k) continue;
+      const int slot = g.slots[t * g.top_k + j0 + u];
+      if ((unsigned)slot >= (unsigned)g.n_rows) continue;
+      w[u] = g.weights ? g.weights[t * g.top_k + j0 + u] : 1.0f;
+      r[u] = y[(size_t)slot * vpr + v];
+    }
+#pragma unroll
+    for (int u = 0; u < kCombineAhead; ++u) {
+      float f[8];
+      unpack8(r[u], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] = fmaf(w[u], f[e], s[e]);
+    }
+  }
+  reinterpret_cast<Raw8<T>*>(g.out)[(size_t)t * vpr + v] = pack8(s, T());
+}
+
+// dy[slot] = weight dout[t],  dweights[t, j] = <dout[t], y[slot]>: a wave to a
+// token, eight choices at a time.
+template <typename T>
+__global__ __launch_bounds__(256) void combine_backward_kernel(const CombineGradArgs g) {
+  const int lane = threadIdx.x & 63, vpr = g.cols / 8;
+  const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= g.tokens) return;
+  const Raw8<T>* y = reinterpret_cast<const Raw8<T>*>(g.y);
+  const Raw8<T>* dout = reinterpret_cast<const Raw8<T>*>(g.dout) + (size_t)t * vpr;
+  Raw8<T>* dy = reinterpret_cast<Raw8<T>*>(g.dy);
+  for (int j0 = 0; j0 < g.top_k; j0 += kCombineAhead) {
+    int slot[kCombineAhead];
+    float w[kCombineAhead], dot[kCombineAhead];
+#pragma unroll
+    for (int u = 0; u < kCombineAhead; ++u) {
+      const bool on = j0 + u < g.top_k;
+      slot[u] = on ? g.slots[t * g.top_k + j0 + u] : -1;
+      if ((unsigned)slot[u] >= (unsigned)g.n_rows) slot[u] = -1;
+      w[u] = on && g.weights ? g.weights[t * g.top_k + j0 + u] : 1.0f;
+      dot[u] = 0.0f;
+    }
+    for (int v = lane; v < vpr; v += 64) {
+      float d[8];
+      unpack8(dout[v], d);
+      Raw8<T> r[kCombineAhead];
+      if (g.dweights) {
+#pragma unroll
+        for (int u = 0; u < kCombineAhead; ++u) {
+          r[u] = Raw8<T>{};
+          if (slot[u] >= 0) r[u] = y[(size_t)slot[u] * vpr + v];
+        }
+      }
+      if (dy) {
+#pragma unroll
+        for (int u = 0; u < kCombineAhead; ++u) {
+          if (slot[u] < 0) continue;
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = w[u] * d[e];
+          dy[(size_t)slot[u] * vpr + v] = pack8(f, T());
+        }
+      }
+      if (g.dweights) {
+#pragma unroll
+        for (int u = 0; u < kCombineAhead; ++u) {
+          float f[8];
+          unpack8(r[u], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot[u] = fmaf(f[e], d[e], dot[u]);
+        }
+      }
+    }
+    if (g.dweights) {
+#pragma unroll
+      for (int u = 0; u < kCombineAhead; ++u) {
+        const float s = wave_sum(dot[u]);
+        if (lane == 0 && j0 + u < g.top_k) g.dweights[t * g.top_k + j0 + u] = slot[u] >= 0 ? s : 0.0f;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_experts(int dtype, ExpertsMode mode, const ExpertsArgs& g, hipStream_t st) {
+  switch (mode) {
+    case EXP_PRODUCT: return launch_mode<EXP_PRODUCT>(dtype, g, st);
+    case EXP_INPUT_GRAD: return launch_mode<EXP_INPUT_GRAD>(dtype, g, st);
+    default: return launch_mode<EXP_WEIGHT_GRAD>(dtype, g, st);
+  }
+}
+
+std::string experts_variant(int dtype, ExpertsMode, const ExpertsArgs&) {
+  return dtype == 1 ? "tile=128x128" : "tile=128x128";
+}
+
+hipError_t launch_combine(int dtype, const CombineArgs& g, hipStream_t st) {
+  const int vpr = g.cols / 8, tpb = vpr >= 256 ? 1 : 256 / vpr;
+  const dim3 grid((unsigned)((g.tokens + tpb - 1) / tpb), (unsigned)(vpr >= 256 ? (vpr + 255) / 256 : 1));
+  if (dtype == 1) dispatch(combine_kernel<bf16>, grid, dim3(256), st, g);
+  else dispatch(combine_kernel<float>, grid, dim3(256), st, g);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_backward(int dtype, const CombineGradArgs& g, hipStream_t st) {
+  const dim3 grid((unsigned)((g.tokens + 3) / 4));
+  if (dtype == 1) dispatch(combine_backward_kernel<bf16>, grid, dim3(256), st, g);
+  else dispatch(combine_backward_kernel<float>, grid, dim3(256), st, g);
+  return hipGetLastError();
+}
+
+}  // namespace ns

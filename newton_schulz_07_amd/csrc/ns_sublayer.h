@@ -1,0 +1,152 @@
+// ns_sublayer.h - arguments, launch rules and launch interface of the
+// mixture-of-experts sublayer's kernels: layer norm, routing, the experts'
+// products, combine.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "../../include/ns_hip.h"
+#include "ns_layout.h"
+
+namespace ns {
+
+// ------------------------------------------------------------ layer norm
+
+struct LayerNormArgs {
+  const void* x;  // [rows, cols], rows ldx elements apart
+  const void *w, *b;  // [cols] or null
+  void* y;        // [rows, cols] contiguous
+  float *mean, *rstd;  // [rows] or null
+  long long rows, ldx;
+  int cols, param_dtype;
+  float eps;
+};
+struct LayerNormGradArgs {
+  const void *dy, *x;  // rows lddy / ldx elements apart
+  const void* w;       // [cols] or null
+  const float *mean, *rstd;
+  void* dx;            // [rows, cols] contiguous, or null
+  void *dw, *db;       // [cols] or null
+  float* partials;     // [blocks][2][cols], null if neither dw nor db is wanted
+  long long rows, lddy, ldx;
+  int cols, param_dtype;
+};
+
+// A row is held by tpr threads of vpt vectors of 8 elements (vpt 0: too long
+// for the registers).  A wave holds up to 2048 columns and needs no barrier
+// for its sums; longer rows take a whole block.
+struct NormShape {
+  int tpr, vpt;
+};
+inline NormShape norm_shape(int cols) {
+  const int nv = (cols + 7) / 8;
+  return nv <= 64     ? NormShape{64, 1}
+         : nv <= 128  ? NormShape{64, 2}
+         : nv <= 256  ? NormShape{64, 4}
+         : nv <= 512  ? NormShape{256, 2}
+         : nv <= 1024 ? NormShape{256, 4}
+         : nv <= 4096 ? NormShape{1024, 4}
+                      : NormShape{1024, 0};
+}
+constexpr int kNormForwardBlocks = 2048, kNormBackwardBlocks = 512;
+inline long long norm_blocks(long long rows, NormShape s, long long most) {
+  const long long need = s.tpr == 64 ? (rows + 3) / 4 : rows;
+  return need < most ? need : most;
+}
+// Blocks of the backward pass: each has 8 bytes of partial sums per column,
+// so long rows get fewer (at most 256 MiB of partials).
+inline int norm_backward_blocks(long long rows, int cols) {
+  long long most = kNormBackwardBlocks;
+  const long long fit = (1ll << 28) / (8ll * cols);
+  if (most > fit) most = fit > 0 ? fit : 1;
+  return (int)norm_blocks(rows, norm_shape(cols), most);
+}
+
+hipError_t launch_layer_norm(int dtype, const LayerNormArgs& g, hipStream_t st);
+// blocks: norm_backward_blocks (0 with no rows: dw and db become zero)
+hipError_t launch_layer_norm_backward(int dtype, const LayerNormGradArgs& g, int blocks, hipStream_t st);
+
+// --------------------------------------------------------------- routing
+
+constexpr int kMaxExperts = 1024, kMaxTopK = 64, kMaxGroups = 64;
+constexpr int kRouteWaves = 16;       // waves, and tokens, of a routing block
+constexpr int kRouteSingleTokens = 64;  // up to here one block does it all
+
+struct RouteArgs {
+  const void* logits;  // [tokens, experts], rows ld elements apart
+  const float* bias;   // [experts] or null
+  int* ids;            // [tokens, top_k]
+  float* weights;      // [tokens, top_k]
+  int *offsets, *rows, *slots;  // [experts + 1], [tokens * top_k], [tokens, top_k]; all null: no plan
+  int* hist;           // workspace [blocks][experts], then [experts] totals
+  long long ld;
+  int tokens, experts, top_k, groups, top_groups, group_best, score, renormalize;
+  float scale;
+};
+struct RouteGradArgs {
+  const void* logits;
+  const int* ids;
+  const float* dweights;
+  void* dlogits;       // [tokens, experts] contiguous
+  long long ld;
+  int tokens, experts, top_k, score, renormalize;
+  float scale;
+};
+inline int route_blocks(int tokens) {
+  return tokens <= kRouteSingleTokens ? 1 : (tokens + kRouteWaves - 1) / kRouteWaves;
+}
+inline size_t route_workspace(int tokens, int experts) {
+  return (size_t)(route_blocks(tokens) + 1) * experts * sizeof(int);
+}
+hipError_t launch_route(int dtype, const RouteArgs& g, hipStream_t st);
+hipError_t launch_route_backward(int dtype, const RouteGradArgs& g, hipStream_t st);
+
+// --------------------------------------------------- the experts' products
+
+// Sorted rows: row i belongs to expert e for offsets[e] <= i < offsets[e + 1].
+// Offsets are device data: they are clamped to [0, n_rows], and a row number
+// outside [0, n_x) reads as a row of zeros.
+enum ExpertsMode : int {
+  EXP_PRODUCT = 0,     // out[i] = x[rows[i]] W_eᵀ
+  EXP_INPUT_GRAD = 1,  // out[i] = dy[i] W_e
+  EXP_WEIGHT_GRAD = 2  // out[e] = sum over e's rows of dy[i]ᵀ x[rows[i]]
+};
+struct ExpertsArgs {
+  const void* x;       // [n_x, fan_in], rows ldx elements apart (product, weight gradient)
+  const void* dy;      // [n_rows, fan_out] (gradients)
+  const void* w;       // [experts, fan_out, fan_in] (product, input gradient)
+  void* out;
+  const int* offsets;  // [experts + 1]
+  const int* rows;     // [n_rows], or null: row i of x
+  long long ldx;
+  int n_x, n_rows, experts, fan_out, fan_in;
+};
+// The kernel instance that launch_experts runs, for ns_query_last_config.
+std::string experts_variant(int dtype, ExpertsMode mode, const ExpertsArgs& g);
+hipError_t launch_experts(int dtype, ExpertsMode mode, const ExpertsArgs& g, hipStream_t st);
+
+// ---------------------------------------------------------------- combine
+
+struct CombineArgs {
+  const void* y;         // [n_rows, cols]
+  const int* slots;      // [tokens, top_k]: rows of y; one outside [0, n_rows) adds nothing
+  const float* weights;  // [tokens, top_k], or null: 1
+  void* out;             // [tokens, cols]
+  int tokens, top_k, n_rows, cols;
+};
+struct CombineGradArgs {
+  const void *dout, *y;
+  const int* slots;
+  const float* weights;
+  void* dy;         // [n_rows, cols], or null
+  float* dweights;  // [tokens, top_k], or null
+  int tokens, top_k, n_rows, cols;
+};
+hipError_t launch_combine(int dtype, const CombineArgs& g, hipStream_t st);
+hipError_t launch_combine_backward(int dtype, const CombineGradArgs& g, hipStream_t st);
+
+}  // namespace ns
