@@ -126,6 +126,7 @@ void record_config(const Plan& p, int steps) {
                            ? "staggered"
                            : "stage-start"));
   t_cfg = buf;
+  ns::t_lazy_cfg.fmt = nullptr;
   if (p.padded)
     t_cfg += " | zero-padded from " + std::to_string(p.urows) + "x" + std::to_string(p.ucols) + " to " +
              std::to_string(p.rows) + "x" + std::to_string(p.cols);
@@ -341,6 +342,7 @@ void record_config_grouped(const std::vector<Group>& gs, const ns::TileChoice& t
                 launches[0], launches[1], launches[2], tw.bm, tw.bn, tt.bm, tt.bn, tp.bm, tp.bn,
                 tc.lower_only ? " (A read as its lower block triangle)" : "", tr.bm, tr.bn);
   t_cfg = buf;
+  ns::t_lazy_cfg.fmt = nullptr;
   t_cfg += " | stacks:";
   for (size_t i = 0; i < gs.size() && i < 64; ++i) {
     const Plan& p = gs[i].p;

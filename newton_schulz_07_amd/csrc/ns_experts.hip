@@ -79,6 +79,40 @@ __device__ __forceinline__ Tile find_tile(const ExpertsArgs& g, int bm, int upto
   return t;
 }
 
+// Weight gradient: workgroup w -> expert and tile q of its T tiles.  Experts
+// differ in their rows and so in the time of their tiles; each XCD (w mod 8)
+// therefore takes about an eighth of the tiles of EVERY expert, the remainder
+// of T / 8 dealt out so that it has T tiles of every 8 experts.  (With one
+// contiguous range of tiles for each XCD the one with the largest experts
+// ends last.)
+__device__ __forceinline__ int expert_tile(int w, int experts, int T, int* q) {
+  const int x = w % 8, octet = w / 8 / T;
+  if (octet < experts / 8) {
+    int m = w / 8 - octet * T, o = 0;
+    for (int i = 0;; ++i) {
+      const int p = T / 8 + (((x - o + 8) % 8) < T % 8 ? 1 : 0);
+      if (m < p || i == 7) {
+        int before = 0;  // XCDs below x that take one more tile of this expert
+        for (int y = 0; y < x; ++y) before += ((y - o + 8) % 8) < T % 8 ? 1 : 0;
+        *q = x * (T / 8) + before + m;
+        return octet * 8 + i;
+      }
+      m -= p;
+      o = (o + T % 8) % 8;
+    }
+  }
+  const int e0 = experts / 8 * 8, lin = xcd_remap(w - e0 * T, (experts - e0) * T);
+  *q = lin % T;
+  return e0 + lin / T;
+}
+
+// The descriptor, in scalar registers (it is the same in every lane).
+__device__ __forceinline__ i32x4 uniform(i32x4 r) {
+  i32x4 u = {__builtin_amdgcn_readfirstlane(r[0]), __builtin_amdgcn_readfirstlane(r[1]),
+             __builtin_amdgcn_readfirstlane(r[2]), __builtin_amdgcn_readfirstlane(r[3])};
+  return u;
+}
+
 typedef const __attribute__((address_space(4))) int* ConstInts;  // read with scalar loads
 
 template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, int MODE>
@@ -88,11 +122,11 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   constexpr int EPC = Elem<T>::kChunk, ES = (int)sizeof(T), BK = CPR * EPC;
   constexpr int WTM = BM / WM, WTN = BN / WN, SM = WTM / 32, SN = WTN / 32;
   constexpr int LP = BM * CPR, LQ = BN * CPR, STAGE = LP + LQ;
-  constexpr int NIW = STAGE / 64 / NW;
+  constexpr int NP = LP / 64 / NW, NQ = LQ / 64 / NW, NIW = NP + NQ;  // a wave's loads of a stage
   constexpr int ERC = epi_row_chunks(BN, ES);
   constexpr int RCP = BM / EPC, RCQ = BN / EPC;
   static_assert(WTM % 32 == 0 && WTN % 32 == 0, "wave tile must be whole 32x32 blocks");
-  static_assert(STAGE % (64 * NW) == 0 && (LP / 64) % NIW == 0, "a wave loads one operand");
+  static_assert(LP % (64 * NW) == 0 && LQ % (64 * NW) == 0, "operands must split into whole wave loads");
   static_assert(ST >= 2 && NIW * (ST - 2) < 64, "ring depth");
   __shared__ uint4 lds[lds_chunks(BM, BN, CPR, ST, ES)];
 
@@ -108,13 +142,14 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   int i0, j0;
   if (MODE == EXP_WEIGHT_GRAD) {
     const int tiles_m = (M + BM - 1) / BM, per = tiles_m * tiles_n;
-    const int lin = xcd_remap(blockIdx.x, gridDim.x);
-    const int e = lin / per;
-    int ti, tj;
-    rect_decode(lin - e * per, tiles_m, tiles_n, ti, tj);
+    int q, ti, tj;
+    const int e = expert_tile(blockIdx.x, g.experts, per, &q);
+    rect_decode(q, tiles_m, tiles_n, ti, tj);
     tl.expert = e;
     tl.tile = ti;
     expert_rows(g.offsets, e, g.experts, g.n_rows, &tl.begin, &tl.count);
+    tl.begin = __builtin_amdgcn_readfirstlane(tl.begin);
+    tl.count = __builtin_amdgcn_readfirstlane(tl.count);
     i0 = ti * BM;
     j0 = tj * BN;
   } else {
@@ -132,108 +167,121 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   const int K = MODE == EXP_PRODUCT ? g.fan_in : MODE == EXP_INPUT_GRAD ? g.fan_out : tl.count;
   const int m_end = MODE == EXP_WEIGHT_GRAD ? M : tl.count;
 
-  // Sources.  A wave loads chunks of one operand only.
-  const bool is_p = wave * NIW * 64 < LP;
-  const T* base;       // descriptor base (weight gradient: moved at each stage)
-  size_t bytes;        // descriptor length
-  unsigned off[NIW];   // byte offset at k0 = 0, kOutOfRange for rows and columns past the end
-  unsigned step = BK * ES;
+  // Sources of a wave's loads t of a stage: P for t < NP, then Q.
   const T* W = reinterpret_cast<const T*>(g.w) + (size_t)tl.expert * g.fan_out * g.fan_in;
-  if constexpr (MODE == EXP_WEIGHT_GRAD) {
-    base = is_p ? reinterpret_cast<const T*>(g.dy) + (size_t)tl.begin * g.fan_out
-                : reinterpret_cast<const T*>(g.x) + (g.rows ? 0 : (size_t)tl.begin * g.ldx);
-    bytes = 0;
-  } else if (is_p) {
+  auto src = [&](int t) __attribute__((always_inline)) {
+    return dma_src(t < NP ? wave * NP + t : LP / 64 + wave * NQ + t - NP, lane, BM, BN, CPR, EPC, PNAT, QNAT, ES);
+  };
+  auto lds_of = [&](int slot, int t) __attribute__((always_inline)) {
+    return lds_addr(lds + slot * STAGE + (t < NP ? wave * NP + t : LP / 64 + wave * NQ + t - NP) * 64);
+  };
+
+  // Product and input gradient: byte offsets at k0 = 0, kOutOfRange for rows
+  // and columns past the end, and one descriptor for each operand.
+  constexpr bool WG = MODE == EXP_WEIGHT_GRAD;
+  unsigned off[WG ? 1 : NIW];
+  const unsigned step_q = (unsigned)((QNAT ? BK * g.fan_in : BK) * ES);
+  i32x4 rP{}, rQ{};
+  if constexpr (!WG) {
     const long long ld = MODE == EXP_PRODUCT ? g.ldx : g.fan_out;
     const bool gather = MODE == EXP_PRODUCT && g.rows != nullptr;
-    base = reinterpret_cast<const T*>(MODE == EXP_PRODUCT ? g.x : g.dy) + (gather ? 0 : (tl.begin + i0) * ld);
-    bytes = gather ? ((size_t)(g.n_x - 1) * ld + g.fan_in) * ES
-                   : ((size_t)(min(BM, tl.count - i0) - 1) * ld + K) * ES;
+    const size_t rows = gather ? (size_t)g.n_x : (size_t)min(BM, tl.count - i0);
+    rP = uniform(make_rsrc(reinterpret_cast<const T*>(MODE == EXP_PRODUCT ? g.x : g.dy) + (gather ? 0 : (tl.begin + i0) * ld),
+                           (unsigned)(((rows - 1) * ld + K) * ES)));
+    rQ = uniform(make_rsrc(W, (unsigned)((size_t)g.fan_out * g.fan_in * ES)));
 #pragma unroll
     for (int t = 0; t < NIW; ++t) {
-      const DmaSrc d = dma_src(wave * NIW + t, lane, BM, BN, CPR, EPC, false, QNAT, ES);
-      int r = d.row;
-      bool ok = i0 + r < tl.count;
-      if (gather) {
-        r = ok ? g.rows[tl.begin + i0 + r] : 0;
-        ok = ok && (unsigned)r < (unsigned)g.n_x;
-      } else if (MODE == EXP_PRODUCT) {
-        ok = ok && tl.begin + i0 + r < g.n_x;
+      const DmaSrc d = src(t);
+      if (t < NP) {
+        int r = d.row;
+        bool ok = i0 + r < tl.count;
+        if (gather) {
+          r = ok ? g.rows[tl.begin + i0 + r] : 0;
+          ok = ok && (unsigned)r < (unsigned)g.n_x;
+        } else if (MODE == EXP_PRODUCT) {
+          ok = ok && tl.begin + i0 + r < g.n_x;
+        }
+        off[t] = ok ? (unsigned)(((size_t)r * ld + d.kpos) * ES) : kOutOfRange;
+      } else {
+        const int j = j0 + d.row;
+        off[t] = j >= N ? kOutOfRange
+                        : (unsigned)((QNAT ? (size_t)d.kpos * g.fan_in + j : (size_t)j * g.fan_in + d.kpos) * ES);
       }
-      off[t] = ok ? (unsigned)(((size_t)r * ld + d.kpos) * ES) : kOutOfRange;
-    }
-  } else {
-    base = W;
-    bytes = (size_t)g.fan_out * g.fan_in * ES;
-    if (QNAT) step = (unsigned)(BK * g.fan_in * ES);
-#pragma unroll
-    for (int t = 0; t < NIW; ++t) {
-      const DmaSrc d = dma_src(wave * NIW + t, lane, BM, BN, CPR, EPC, false, QNAT, ES);
-      const int j = j0 + d.row;
-      off[t] = j >= N ? kOutOfRange
-                      : (unsigned)((QNAT ? (size_t)d.kpos * g.fan_in + j : (size_t)j * g.fan_in + d.kpos) * ES);
     }
   }
-  // weight gradient: this wave's k rows of a stage are kr0 .. kr0 + KR - 1,
-  // RPI to an instruction; x's row numbers are read one stage ahead
-  constexpr int RC = BM / EPC, RPI = 64 / RC, KR = NIW * RPI;
-  static_assert(MODE != EXP_WEIGHT_GRAD || (BM == BN && KR <= 16), "square tiles");
-  const int kr0 = MODE == EXP_WEIGHT_GRAD ? (wave * NIW * 64 - (is_p ? 0 : LP)) / RC : 0;
-  int idx[MODE == EXP_WEIGHT_GRAD ? KR : 1];
+
+  // Weight gradient: a load covers 64 / RC k rows of a stage, lane l the one
+  // of number l / RC, at a column that repeats every NC loads (nat_swz sees
+  // the last two bits of the k row in bf16, the last three in fp32).
+  // Columns past the end read the last ones: what they add up to is never
+  // stored.  k rows past the end must be zero: the descriptor ends there, or
+  // the gathered row's offset is out of range.
+  constexpr int RPP = 64 / RCP, RPQ = 64 / RCQ, KRQ = NQ * RPQ;
+  const unsigned ldp = (unsigned)(g.fan_out * ES), ldq = (unsigned)(g.ldx * ES);
+  const bool gather = WG && g.rows != nullptr;
+  constexpr int NC = ES == 2 ? 2 : 4;
+  static_assert(!WG || (NP % NC == 0 && NQ % NC == 0 && NC * RPP % (2 * NC) == 0 && NC * RPQ % (2 * NC) == 0),
+                "columns repeat every NC loads");
+  unsigned colp[WG ? NC : 1], colq[WG ? NC : 1];
+  if constexpr (WG) {
+#pragma unroll
+    for (int t = 0; t < NC; ++t) {
+      colp[t] = (unsigned)(min(i0 + src(t).row, M - EPC) * ES) + (unsigned)(lane / RCP) * ldp;
+      colq[t] = (unsigned)(min(j0 + src(NP + t).row, N - EPC) * ES) + (gather ? 0u : (unsigned)(lane / RCQ) * ldq);
+    }
+  }
+  // x's row numbers of a wave's loads, read one stage ahead; past the expert's rows: none
+  int idx[WG ? KRQ : 1];
   const ConstInts rows_c = (ConstInts)(unsigned long long)(g.rows + (g.rows ? tl.begin : 0));
   auto read_idx = [&](int kt) __attribute__((always_inline)) {
-    if constexpr (MODE == EXP_WEIGHT_GRAD) {
-      if (is_p || g.rows == nullptr || kt * BK + kr0 >= K) return;
-      const int k = kt * BK + kr0;
-      if (k + KR <= K) {
+    if constexpr (WG) {
+      if (!gather || kt * BK >= K) return;
+      const int k = kt * BK + wave * KRQ;
 #pragma unroll
-        for (int r = 0; r < KR; ++r) idx[r] = rows_c[k + r];
-      } else {
-#pragma unroll
-        for (int r = 0; r < KR; ++r) idx[r] = rows_c[min(k + r, K - 1)];
+      for (int r = 0; r < KRQ; ++r) {
+        const int v = rows_c[min(k + r, K - 1)];
+        idx[r] = k + r < K ? v : -1;
       }
     }
   };
 
   auto issue = [&](int kt, int slot) __attribute__((always_inline)) {
     const int k0 = kt * BK;
-    if constexpr (MODE == EXP_WEIGHT_GRAD) {
-      const long long ld = is_p ? (long long)g.fan_out : g.ldx;
-      const bool gather = !is_p && g.rows != nullptr;
-      const int left = K - k0;  // > 0
-      const i32x4 rs = make_rsrc(base + (gather ? 0 : k0 * ld),
-                                 gather ? (unsigned)(((size_t)(g.n_x - 1) * ld + g.fan_in) * ES)
-                                        : (unsigned)(((size_t)(min(BK, left) - 1) * ld + (is_p ? g.fan_out : g.fan_in)) * ES));
+    if constexpr (WG) {
+      const unsigned left = (unsigned)min(BK, K - k0);  // > 0
+      const T* dy = reinterpret_cast<const T*>(g.dy) + (size_t)(tl.begin + k0) * g.fan_out;
+      const T* x = reinterpret_cast<const T*>(g.x) + (gather ? 0 : (size_t)(tl.begin + k0) * g.ldx);
+      const i32x4 p = uniform(make_rsrc(dy, left * ldp));
+      const i32x4 q = uniform(make_rsrc(x, (gather ? (unsigned)g.n_x - 1 : left - 1) * ldq + (unsigned)(g.fan_in * ES)));
 #pragma unroll
       for (int t = 0; t < NIW; ++t) {
-        const DmaSrc d = dma_src(wave * NIW + t, lane, BM, BN, CPR, EPC, true, true, ES);
-        const int c = (is_p ? i0 : j0) + d.row;
-        int r = d.kpos;
-        bool ok = c < (is_p ? M : N) && d.kpos < left;
-        if (!is_p) {
-          if (gather) {
-            r = idx[t * RPI];
-#pragma unroll
-            for (int u = 1; u < RPI; ++u)
-              if (lane / RC == u) r = idx[t * RPI + u];
-            ok = ok && (unsigned)r < (unsigned)g.n_x;
-          } else {
-            ok = ok && tl.begin + k0 + r < g.n_x;
-          }
+        if (t < NP) {
+          dma16(lds_of(slot, t), colp[t % NC] + (unsigned)(wave * NP + t) * RPP * ldp, p);
+          continue;
         }
-        dma16(lds_addr(lds + slot * STAGE + (wave * NIW + t) * 64),
-              ok ? (unsigned)(r * (unsigned)(ld * ES) + (unsigned)(c * ES)) : kOutOfRange, rs);
+        const int u = t - NP;
+        unsigned o;
+        if (gather) {
+          // row offsets in scalars; a lane takes that of its k row
+          auto at = [&](int r) __attribute__((always_inline)) -> unsigned {
+            return (unsigned)idx[r] < (unsigned)g.n_x ? (unsigned)idx[r] * ldq : kOutOfRange;
+          };
+          o = at(u * RPQ);
+#pragma unroll
+          for (int v = 1; v < RPQ; ++v) o = lane / RCQ == v ? at(u * RPQ + v) : o;
+        } else {
+          o = (unsigned)(wave * NQ + u) * RPQ * ldq;
+        }
+        dma16(lds_of(slot, t), o + colq[u % NC], q);
       }
       read_idx(kt + 1);
     } else {
-      const i32x4 rs = make_rsrc(base, (unsigned)bytes);
       const bool whole = k0 + BK <= K;
 #pragma unroll
       for (int t = 0; t < NIW; ++t) {
-        const int kpos = dma_src(wave * NIW + t, lane, BM, BN, CPR, EPC, false, QNAT, ES).kpos;
-        // (an offset out of range stays there: step * kt is below 2^31)
-        dma16(lds_addr(lds + slot * STAGE + (wave * NIW + t) * 64),
-              whole || k0 + kpos < K ? off[t] + (unsigned)kt * step : kOutOfRange, rs);
+        // (an offset out of range stays there: kt steps are below 2^31)
+        const unsigned o = off[t] + (unsigned)kt * (t < NP ? (unsigned)(BK * ES) : step_q);
+        dma16(lds_of(slot, t), whole || k0 + src(t).kpos < K ? o : kOutOfRange, t < NP ? rP : rQ);
       }
     }
   };
@@ -283,12 +331,32 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
       else qf[b] = *reinterpret_cast<const uint4*>(st + kcq[s ^ kc_sigma(b, CPR)] + b * 32 * CPR * 16);
     }
   };
-  auto compute = [&](int slot) __attribute__((always_inline)) {
-    uint4 pf[2][SM], qf[2][SN];
-    load_step(slot, 0, pf[0], qf[0]);
+  // Ring of ST stages: stage kt lives in slot kt % ST, and its loads go out
+  // ST - 1 stages ahead.  The fragments of step s + 1 are read while the MFMAs
+  // of step s run, across the stages' border too: before a stage's last MFMAs
+  // a wave waits for its own loads of the next stage, and the barrier there
+  // publishes every wave's and certifies that this stage's slot is read out.
+  const int nk = (K + BK - 1) / BK;
+  uint4 pf[2][SM], qf[2][SN];
+  auto wait_stage = [&](int kt) __attribute__((always_inline)) {
+    const int later = nk - 1 - kt;  // stages that may be in flight after kt, at most ST - 2
+    if (later >= ST - 2) wait_vm_lgkm0<NIW * (ST - 2)>();
+    else if (ST > 4 && later == 2) wait_vm_lgkm0<NIW * 2>();
+    else if (ST > 3 && later == 1) wait_vm_lgkm0<NIW * 1>();
+    else wait_vm_lgkm0<0>();
+    ring_barrier();
+  };
+  static_assert(ST <= 5 && KS % 2 == 0, "tail waits; fragment buffers alternate");
+  auto stage = [&](int kt, int u) __attribute__((always_inline)) {
+    if (kt + ST - 1 < nk) issue(kt + ST - 1, (u + ST - 1) % ST);
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      if (s + 1 < KS) load_step(slot, s + 1, pf[(s + 1) & 1], qf[(s + 1) & 1]);
+      if (s + 1 < KS) {
+        load_step(u, s + 1, pf[(s + 1) & 1], qf[(s + 1) & 1]);
+      } else if (kt + 1 < nk) {
+        wait_stage(kt + 1);
+        load_step((u + 1) % ST, 0, pf[0], qf[0]);
+      }
       __builtin_amdgcn_sched_barrier(0);  // keeps these reads ahead of the MFMAs
 #pragma unroll
       for (int a = 0; a < SM; ++a)
@@ -296,24 +364,14 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
         for (int b = 0; b < SN; ++b) mfma_chunk(acc[a][b], qf[s & 1][b], pf[s & 1][a], T());
     }
   };
-
-  // Ring of ST stages: stage kt lives in slot kt % ST; before computing it a
-  // wave waits for its own loads of it, and the barrier publishes every
-  // wave's and certifies that slot (kt - 1) % ST is no longer read.
-  const int nk = (K + BK - 1) / BK;
-  auto stage = [&](int kt, int u) __attribute__((always_inline)) {
-    const int after = nk - 1 - kt;
-    if (after >= ST - 2) wait_vm_lgkm0<NIW * (ST - 2)>();
-    else wait_vm_lgkm0<0>();
-    ring_barrier();
-    if (kt + ST - 1 < nk) issue(kt + ST - 1, (u + ST - 1) % ST);
-    compute(u);
-  };
-  static_assert(ST <= 3, "the tail wait assumes at most one later stage in flight");
   read_idx(0);
 #pragma unroll
   for (int s = 0; s < ST - 1; ++s)
     if (s < nk) issue(s, s);
+  if (nk > 0) {
+    wait_stage(0);
+    load_step(0, 0, pf[0], qf[0]);
+  }
   int kt0 = 0;
   for (; kt0 + ST <= nk; kt0 += ST) {
 #pragma unroll
@@ -369,10 +427,22 @@ hipError_t launch_tiles(const ExpertsArgs& g, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int MODE>
+#define NS_EXPERTS_WIDE 256, 256, 2, 4, 8, 2, 1
+#define NS_EXPERTS_LONG 128, 256, 2, 2, 4, 3, 2
+#define NS_EXPERTS_F32 128, 128, 2, 2, 8, 3, 1
+
+// Rows enough to fill 256-row tiles: an expert's last tile is half empty on
+// average.
+bool wide_tiles(ExpertsMode mode, const ExpertsArgs& g) {
+  return mode == EXP_PRODUCT && g.n_rows / g.experts >= 256;
+}
+
+template <ExpertsMode MODE>
 hipError_t launch_mode(int dtype, const ExpertsArgs& g, hipStream_t st) {
-  if (dtype == 1) return launch_tiles<bf16, 128, 128, 2, 4, 8, 2, 2, MODE>(g, st);
-  return launch_tiles<float, 128, 128, 2, 2, 8, 3, 1, MODE>(g, st);
+  if (dtype != 1) return launch_tiles<float, NS_EXPERTS_F32, MODE>(g, st);
+  if constexpr (MODE == EXP_PRODUCT)
+    if (wide_tiles(MODE, g)) return launch_tiles<bf16, NS_EXPERTS_WIDE, MODE>(g, st);
+  return launch_tiles<bf16, NS_EXPERTS_LONG, MODE>(g, st);
 }
 
 // ---------------------------------------------------------------- combine
@@ -493,8 +563,15 @@ hipError_t launch_experts(int dtype, ExpertsMode mode, const ExpertsArgs& g, hip
   }
 }
 
-std::string experts_variant(int dtype, ExpertsMode, const ExpertsArgs&) {
-  return dtype == 1 ? "tile=128x128" : "tile=128x128";
+const char* experts_config(int dtype, ExpertsMode mode, const ExpertsArgs& g) {
+#define NS_TEXT(NAME, TILE) NAME ": dtype=%s rows=%lld experts=%lld fan_out=%lld fan_in=%lld | tile=" TILE
+#define NS_TILES(NAME)                                                                               \
+  dtype != 1 ? NS_TEXT(NAME, "128x128") : wide_tiles(mode, g) ? NS_TEXT(NAME, "256x256") : NS_TEXT(NAME, "128x256")
+  return mode == EXP_PRODUCT      ? (NS_TILES("experts product"))
+         : mode == EXP_INPUT_GRAD ? (NS_TILES("experts input gradient"))
+                                  : (NS_TILES("experts weight gradient"));
+#undef NS_TILES
+#undef NS_TEXT
 }
 
 hipError_t launch_combine(int dtype, const CombineArgs& g, hipStream_t st) {

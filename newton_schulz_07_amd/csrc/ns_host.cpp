@@ -2,6 +2,7 @@
 // entry points that report on it (errors, workspace, timing).
 #include "ns_host.h"
 
+#include <cstdio>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -14,6 +15,7 @@ namespace ns {
 
 thread_local std::string t_err;
 thread_local std::string t_cfg;
+thread_local Config t_lazy_cfg;
 thread_local bool t_untimed = false;
 std::atomic<int> g_poison{0};
 
@@ -211,6 +213,13 @@ const char* ns_status_string(int status) {
 const char* ns_last_error(void) { return t_err.c_str(); }
 
 int ns_query_last_config(char* buf, size_t n) {
+  if (t_lazy_cfg.fmt != nullptr) {
+    const Config& c = t_lazy_cfg;
+    char text[512];
+    std::snprintf(text, sizeof(text), c.fmt, c.text, c.v[0], c.v[1], c.v[2], c.v[3], c.v[4], c.v[5], c.v[6], c.v[7]);
+    t_cfg = text;
+    t_lazy_cfg.fmt = nullptr;
+  }
   if (buf != nullptr && n > 0) {
     std::strncpy(buf, t_cfg.c_str(), n - 1);
     buf[n - 1] = '\0';

@@ -23,6 +23,20 @@ extern thread_local std::string t_cfg;  // ns_query_last_config
 extern thread_local bool t_untimed;
 extern std::atomic<int> g_poison;       // ns_set_workspace_poison
 
+// The same as a format of one text and up to eight numbers, filled in only
+// when ns_query_last_config asks (it counts beside a short launch).
+struct Config {
+  const char* fmt = nullptr;
+  const char* text = "";
+  long long v[8] = {};
+};
+extern thread_local Config t_lazy_cfg;  // fmt null: t_cfg holds the text
+template <typename... A>
+void set_config(const char* fmt, const char* text, A... v) {
+  static_assert(sizeof...(v) <= 8, "at most eight numbers");
+  t_lazy_cfg = Config{fmt, text, {(long long)v...}};
+}
+
 int fail(int status, const std::string& msg);
 int check_hip(hipError_t e, const char* what);
 int check_dtype(int dtype);

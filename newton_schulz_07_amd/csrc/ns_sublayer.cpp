@@ -2,8 +2,6 @@
 // points: argument checks, workspace, launches.
 #include "ns_sublayer.h"
 
-#include <cstdio>
-
 #include "ns_host.h"
 #include "ns_kernels.h"
 #include "ns_plan.h"
@@ -70,13 +68,6 @@ int poison(char* ws, size_t bytes, hipStream_t st) {
 
 const char* type_name(int dtype) { return dtype == NS_DTYPE_BF16 ? "bf16" : "fp32"; }
 
-template <typename... A>
-void config(const char* fmt, A... args) {
-  char buf[512];
-  std::snprintf(buf, sizeof(buf), fmt, args...);
-  t_cfg = buf;
-}
-
 int check_route(int64_t tokens, int64_t experts, int64_t top_k, int64_t ld, int score, int dtype) {
   if (int s = check_dtype(dtype)) return s;
   if (int s = check_rows(tokens, "tokens")) return s;
@@ -122,9 +113,7 @@ int check_x(const void* x, int64_t ldx, int64_t n_x, const void* rows, int64_t n
 int run_experts(ExpertsMode mode, const char* what, const ExpertsArgs& g, int dtype, hipStream_t st) {
   const int s = check_hip(timed_launch(NS_KIND_EXPERTS, st, [&] { return launch_experts(dtype, mode, g, st); }), what);
   if (s) return s;
-  config("%s: dtype=%s rows=%d experts=%d fan_out=%d fan_in=%d%s | %s", what, type_name(dtype), g.n_rows, g.experts,
-         g.fan_out, g.fan_in, mode != EXP_INPUT_GRAD && g.rows ? " gathered" : "",
-         experts_variant(dtype, mode, g).c_str());
+  set_config(experts_config(dtype, mode, g), type_name(dtype), g.n_rows, g.experts, g.fan_out, g.fan_in);
   return NS_OK;
 }
 
@@ -159,8 +148,8 @@ int ns_layer_norm(const void* x, int64_t ldx, const void* weight, const void* bi
                           "layer norm launch"))
       return s;
     const NormShape n = norm_shape((int)cols);
-    config("layer norm: dtype=%s rows=%lld cols=%lld | %d threads x %d vectors of 8 per row", type_name(dtype),
-           (long long)rows, (long long)cols, n.tpr, n.vpt);
+    set_config("layer norm: dtype=%s rows=%lld cols=%lld | %lld threads x %lld vectors of 8 per row", type_name(dtype),
+           rows, cols, n.tpr, n.vpt);
     return NS_OK;
   });
 }
@@ -208,8 +197,8 @@ int ns_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t 
                           "layer norm backward launch"))
       return s;
     const NormShape n = norm_shape((int)cols);
-    config("layer norm backward: dtype=%s rows=%lld cols=%lld | %d threads x %d vectors of 8 per row, %d blocks",
-           type_name(dtype), (long long)rows, (long long)cols, n.tpr, n.vpt, blocks);
+    set_config("layer norm backward: dtype=%s rows=%lld cols=%lld | %lld threads x %lld vectors of 8 per row, %lld blocks",
+           type_name(dtype), rows, cols, n.tpr, n.vpt, blocks);
     return NS_OK;
   });
 }
@@ -249,16 +238,17 @@ int ns_route(const void* logits, int64_t ld, const float* bias, int32_t* ids, fl
     hipStream_t st = static_cast<hipStream_t>(stream);
     char* ws = nullptr;
     const size_t bytes = route_workspace((int)tokens, (int)experts);
-    if (plan && route_blocks((int)tokens) > 1) {
+    if (plan && bytes > 0) {
       if (int s = get_workspace(st, bytes, &ws)) return s;
       if (int s = poison(ws, bytes, st)) return s;
     }
     RouteArgs g{logits, bias, ids, weights, offsets, rows, slots, reinterpret_cast<int*>(ws), ld, (int)tokens,
-                (int)experts, (int)top_k, (int)groups, (int)top_groups, group_best, score, renormalize != 0, scale};
+                (int)experts, (int)top_k, (int)groups, (int)top_groups, group_best, score, renormalize != 0,
+                route_shape((int)tokens, (int)experts).hist_ld, scale};
     if (int s = check_hip(timed_launch(NS_KIND_ROUTE, st, [&] { return launch_route(dtype, g, st); }), "route launch"))
       return s;
-    config("route: dtype=%s tokens=%d experts=%d top_k=%d groups=%d/%d | keys in %d bits, %d blocks", type_name(dtype),
-           g.tokens, g.experts, g.top_k, g.top_groups, g.groups, bias || groups > 1 ? 64 : 32, route_blocks(g.tokens));
+    set_config("route: dtype=%s tokens=%lld experts=%lld top_k=%lld groups=%lld/%lld | keys in %lld bits, %lld blocks", type_name(dtype),
+           g.tokens, g.experts, g.top_k, g.top_groups, g.groups, bias || groups > 1 ? 64 : 32, route_shape(g.tokens, g.experts).blocks);
     return NS_OK;
   });
 }
@@ -284,7 +274,7 @@ int ns_route_backward(const void* logits, int64_t ld, const int32_t* ids, const 
     if (int s = check_hip(timed_launch(NS_KIND_ROUTE, st, [&] { return launch_route_backward(dtype, g, st); }),
                           "route backward launch"))
       return s;
-    config("route backward: dtype=%s tokens=%d experts=%d top_k=%d", type_name(dtype), g.tokens, g.experts, g.top_k);
+    set_config("route backward: dtype=%s tokens=%lld experts=%lld top_k=%lld", type_name(dtype), g.tokens, g.experts, g.top_k);
     return NS_OK;
   });
 }
@@ -380,7 +370,7 @@ int ns_experts_combine(const void* y, const int32_t* slots, const float* weights
     if (int s = check_hip(timed_launch(NS_KIND_COMBINE, st, [&] { return launch_combine(dtype, g, st); }),
                           "combine launch"))
       return s;
-    config("experts combine: dtype=%s tokens=%d top_k=%d cols=%d", type_name(dtype), g.tokens, g.top_k, g.cols);
+    set_config("experts combine: dtype=%s tokens=%lld top_k=%lld cols=%lld", type_name(dtype), g.tokens, g.top_k, g.cols);
     return NS_OK;
   });
 }
@@ -414,7 +404,7 @@ int ns_experts_combine_backward(const void* dout, const void* y, const int32_t* 
     if (int s = check_hip(timed_launch(NS_KIND_COMBINE, st, [&] { return launch_combine_backward(dtype, g, st); }),
                           "combine backward launch"))
       return s;
-    config("experts combine backward: dtype=%s tokens=%d top_k=%d cols=%d", type_name(dtype), g.tokens, g.top_k,
+    set_config("experts combine backward: dtype=%s tokens=%lld top_k=%lld cols=%lld", type_name(dtype), g.tokens, g.top_k,
            g.cols);
     return NS_OK;
   });

@@ -7,8 +7,6 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <string>
-
 #include "../../include/ns_hip.h"
 #include "ns_layout.h"
 
@@ -73,8 +71,9 @@ hipError_t launch_layer_norm_backward(int dtype, const LayerNormGradArgs& g, int
 // --------------------------------------------------------------- routing
 
 constexpr int kMaxExperts = 1024, kMaxTopK = 64, kMaxGroups = 64;
-constexpr int kRouteWaves = 16;       // waves, and tokens, of a routing block
+constexpr int kRouteWaves = 16;        // waves of a routing block, at most
 constexpr int kRouteSingleTokens = 64;  // up to here one block does it all
+constexpr int kRouteUnscannedBlocks = 256;
 
 struct RouteArgs {
   const void* logits;  // [tokens, experts], rows ld elements apart
@@ -82,10 +81,11 @@ struct RouteArgs {
   int* ids;            // [tokens, top_k]
   float* weights;      // [tokens, top_k]
   int *offsets, *rows, *slots;  // [experts + 1], [tokens * top_k], [tokens, top_k]; all null: no plan
-  int* hist;           // workspace [blocks][experts], then [experts] totals
+  int* hist;           // workspace [blocks][hist_ld] counts, then [hist_ld] totals
   long long ld;
-  int tokens, experts, top_k, groups, top_groups, group_best, score, renormalize;
+  int tokens, experts, top_k, groups, top_groups, group_best, score, renormalize, hist_ld;
   float scale;
+  bool vec, vec_bias;  // logits, bias as whole vectors (set at the launch)
 };
 struct RouteGradArgs {
   const void* logits;
@@ -95,12 +95,19 @@ struct RouteGradArgs {
   long long ld;
   int tokens, experts, top_k, score, renormalize;
   float scale;
+  bool vec, vec_out;
 };
-inline int route_blocks(int tokens) {
-  return tokens <= kRouteSingleTokens ? 1 : (tokens + kRouteWaves - 1) / kRouteWaves;
+// A token takes 16 lanes of a wave up to 256 experts, then all 64.
+struct RouteShape {
+  int tokens_per_wave, blocks, hist_ld;
+};
+inline RouteShape route_shape(int tokens, int experts) {
+  const int tpw = experts <= 256 ? 4 : 1, tb = kRouteWaves * tpw;
+  return RouteShape{tpw, tokens <= kRouteSingleTokens ? 1 : (int)(((long long)tokens + tb - 1) / tb), (experts + 3) / 4 * 4};
 }
 inline size_t route_workspace(int tokens, int experts) {
-  return (size_t)(route_blocks(tokens) + 1) * experts * sizeof(int);
+  const RouteShape r = route_shape(tokens, experts);
+  return r.blocks > 1 ? (size_t)(r.blocks + 1) * r.hist_ld * sizeof(int) : 0;
 }
 hipError_t launch_route(int dtype, const RouteArgs& g, hipStream_t st);
 hipError_t launch_route_backward(int dtype, const RouteGradArgs& g, hipStream_t st);
@@ -125,8 +132,9 @@ struct ExpertsArgs {
   long long ldx;
   int n_x, n_rows, experts, fan_out, fan_in;
 };
-// The kernel instance that launch_experts runs, for ns_query_last_config.
-std::string experts_variant(int dtype, ExpertsMode mode, const ExpertsArgs& g);
+// What launch_experts runs, for ns_query_last_config: a format of the type's
+// name, n_rows, experts, fan_out and fan_in.
+const char* experts_config(int dtype, ExpertsMode mode, const ExpertsArgs& g);
 hipError_t launch_experts(int dtype, ExpertsMode mode, const ExpertsArgs& g, hipStream_t st);
 
 // ---------------------------------------------------------------- combine

@@ -35,14 +35,22 @@ class Routing(NamedTuple):
     slots: torch.Tensor     # int32 [..., top_k]
 
 
-def _call(name, dev, *args):
-    """lib().name(*args, stream) on device `dev` and its current stream."""
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+_stream_of = torch._C._cuda_getCurrentRawStream  # the device's current stream, without an object around it
+_current_device = torch._C._cuda_getDevice
+_functions = {}
+
+
+def _call(name, like, *args):
+    """lib().name(*args, stream) on the device of `like` and its current stream."""
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(lib(), name)
+    dev = like.get_device()
+    if _current_device() == dev:
+        status = fn(*args, _stream_of(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+            status = fn(*args, _stream_of(dev))
     if status:
         _check(status)
 
@@ -65,19 +73,27 @@ def _rows_of(t, name):
 
 def _dense(t, name, like=None, dtype=None, shape=None):
     """t, checked: on the GPU (of `like`), contiguous, of this dtype and shape."""
+    if (t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype == dtype) and (shape is None or t.shape == shape)
+            and (like is None or t.get_device() == like.get_device())):
+        return t
     if not t.is_cuda or (like is not None and t.device != like.device):
         raise ValueError(f"{name} must be a tensor on {'the GPU' if like is None else like.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _out(t, name, like, dtype, shape):
-    return like.new_empty(shape, dtype=dtype) if t is None else _dense(t, name, like, dtype, shape)
+    # (sizes one by one: torch takes longer over a tuple)
+    return torch.empty(*shape, dtype=dtype, device=like.device) if t is None else _dense(t, name, like, dtype, shape)
+
+
+def _out_like(t, name, like):
+    if t is None and like.is_contiguous():
+        return torch.empty_like(like)
+    return _out(t, name, like, like.dtype, like.shape)
 
 
 def _code(dtype):
@@ -108,11 +124,11 @@ def ns_layer_norm(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=N
         _dense(weight, "weight", x, None, (cols,))
     if bias is not None:
         _dense(bias, "bias", x, p.dtype, (cols,))
-    y = _out(y, "y", x, x.dtype, x.shape)
+    y = _out_like(y, "y", x)
     mean = _out(mean, "mean", x, torch.float32, (rows,))
     rstd = _out(rstd, "rstd", x, torch.float32, (rows,))
     dt = _code(x.dtype)
-    _call("ns_layer_norm", x.device, x.data_ptr(), ld, _ptr(weight), _ptr(bias), y.data_ptr(), mean.data_ptr(),
+    _call("ns_layer_norm", x, x.data_ptr(), ld, _ptr(weight), _ptr(bias), y.data_ptr(), mean.data_ptr(),
           rstd.data_ptr(), rows, cols, dt, dt if p is None else _code(p.dtype), eps)
     return y, mean, rstd
 
@@ -136,8 +152,8 @@ def ns_layer_norm_backward(dy, x, weight, mean, rstd, bias=True, dx=None, dweigh
         dbias = _out(dbias, "dbias", x, pt, (cols,))
     elif dbias is not None:
         raise ValueError("dbias with bias=False")
-    dx = _out(dx, "dx", x, x.dtype, x.shape)
-    _call("ns_layer_norm_backward", x.device, dy.data_ptr(), ldd, x.data_ptr(), ld, _ptr(weight), mean.data_ptr(),
+    dx = _out_like(dx, "dx", x)
+    _call("ns_layer_norm_backward", x, dy.data_ptr(), ldd, x.data_ptr(), ld, _ptr(weight), mean.data_ptr(),
           rstd.data_ptr(), dx.data_ptr(), _ptr(dweight), _ptr(dbias), rows, cols, _code(x.dtype),
           _code(pt))
     return dx, dweight, dbias
@@ -166,16 +182,15 @@ def ns_route(logits, top_k, bias=None, groups=1, top_groups=1, group_best=2, sco
     code = _score(score)
     if bias is not None:
         _dense(bias, "bias", logits, torch.float32, (experts,))
-    shape = (*logits.shape[:-1], top_k)
-    n = tokens * max(int(top_k), 0)
-    # one allocation for the int32 outputs: ids, rows, slots, offsets
-    ints = logits.new_empty((3 * n + experts + 1) if plan else n, dtype=torch.int32)
-    ids = ints[:n].view(shape)
-    weights = logits.new_empty(shape, dtype=torch.float32)
-    rows = ints[n:2 * n] if plan else None
-    slots = ints[2 * n:3 * n].view(shape) if plan else None
-    offsets = ints[3 * n:] if plan else None
-    _call("ns_route", logits.device, logits.data_ptr(), ld, _ptr(bias), ids.data_ptr(), weights.data_ptr(),
+    dev = logits.device
+    ids = torch.empty(*logits.shape[:-1], top_k, dtype=torch.int32, device=dev)
+    weights = torch.empty(*logits.shape[:-1], top_k, dtype=torch.float32, device=dev)
+    offsets = rows = slots = None
+    if plan:
+        slots = torch.empty_like(ids)
+        rows = torch.empty(tokens * top_k, dtype=torch.int32, device=dev)
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+    _call("ns_route", logits, logits.data_ptr(), ld, _ptr(bias), ids.data_ptr(), weights.data_ptr(),
           _ptr(offsets), _ptr(rows), _ptr(slots), tokens, experts, top_k, groups, top_groups, group_best, code,
           1 if renormalize else 0, scale, _code(logits.dtype))
     return Routing(ids, weights, offsets, rows, slots)
@@ -189,8 +204,8 @@ def ns_route_backward(logits, ids, dweights, score="softmax", renormalize=True, 
     if ids.shape[:-1] != logits.shape[:-1]:
         raise ValueError("ids must have logits' leading shape")
     _dense(dweights, "dweights", logits, torch.float32, ids.shape)
-    dlogits = _out(dlogits, "dlogits", logits, logits.dtype, logits.shape)
-    _call("ns_route_backward", logits.device, logits.data_ptr(), ld, ids.data_ptr(), dweights.data_ptr(),
+    dlogits = _out_like(dlogits, "dlogits", logits)
+    _call("ns_route_backward", logits, logits.data_ptr(), ld, ids.data_ptr(), dweights.data_ptr(),
           dlogits.data_ptr(), tokens, experts, ids.shape[-1], code, 1 if renormalize else 0, scale,
           _code(logits.dtype))
     return dlogits
@@ -221,7 +236,7 @@ def ns_experts_product(x, w, offsets, rows=None, y=None):
     if w_in != fan_in:
         raise ValueError(f"w takes rows of {w_in}, x has rows of {fan_in}")
     y = _out(y, "y", x, x.dtype, (n_rows, fan_out))
-    _call("ns_experts_product", x.device, x.data_ptr(), ld, n_x, _ptr(rows), w.data_ptr(), offsets.data_ptr(),
+    _call("ns_experts_product", x, x.data_ptr(), ld, n_x, _ptr(rows), w.data_ptr(), offsets.data_ptr(),
           y.data_ptr(), n_rows, experts, fan_out, fan_in, _code(x.dtype))
     return y
 
@@ -234,7 +249,7 @@ def ns_experts_input_grad(dy, w, offsets, dx=None):
     _dense(dy, "dy", w, None, (n_rows, fan_out))
     _dense(offsets, "offsets", dy, torch.int32, (experts + 1,))
     dx = _out(dx, "dx", dy, dy.dtype, (n_rows, fan_in))
-    _call("ns_experts_input_grad", dy.device, dy.data_ptr(), w.data_ptr(), offsets.data_ptr(), dx.data_ptr(), n_rows,
+    _call("ns_experts_input_grad", dy, dy.data_ptr(), w.data_ptr(), offsets.data_ptr(), dx.data_ptr(), n_rows,
           experts, fan_out, fan_in, _code(dy.dtype))
     return dx
 
@@ -249,7 +264,7 @@ def ns_experts_weight_grad(dy, x, offsets, rows=None, dw=None):
     fan_out = dy.shape[1]
     _dense(dy, "dy", x, x.dtype, (n_rows, fan_out))
     dw = _out(dw, "dw", x, x.dtype, (experts, fan_out, fan_in))
-    _call("ns_experts_weight_grad", x.device, dy.data_ptr(), x.data_ptr(), ld, n_x, _ptr(rows), offsets.data_ptr(),
+    _call("ns_experts_weight_grad", x, dy.data_ptr(), x.data_ptr(), ld, n_x, _ptr(rows), offsets.data_ptr(),
           dw.data_ptr(), n_rows, experts, fan_out, fan_in, _code(x.dtype))
     return dw
 
@@ -276,7 +291,7 @@ def ns_experts_combine(y, slots, weights=None, out=None):
     tokens, top_k = _slots_of(slots, weights, y)
     n_rows, cols = y.shape
     out = _out(out, "out", y, y.dtype, (*slots.shape[:-1], cols))
-    _call("ns_experts_combine", y.device, y.data_ptr(), slots.data_ptr(), _ptr(weights), out.data_ptr(), tokens,
+    _call("ns_experts_combine", y, y.data_ptr(), slots.data_ptr(), _ptr(weights), out.data_ptr(), tokens,
           top_k, n_rows, cols, _code(y.dtype))
     return out
 
@@ -289,11 +304,11 @@ def ns_experts_combine_backward(dout, y, slots, weights=None, dy=None, dweights=
     tokens, top_k = _slots_of(slots, weights, y)
     n_rows, cols = y.shape
     _dense(dout, "dout", y, y.dtype, (*slots.shape[:-1], cols))
-    dy = _out(dy, "dy", y, y.dtype, (n_rows, cols))
+    dy = _out_like(dy, "dy", y)
     if weights is not None:
-        dweights = _out(dweights, "dweights", y, torch.float32, slots.shape)
+        dweights = _out_like(dweights, "dweights", weights)
     elif dweights is not None:
         raise ValueError("dweights without weights")
-    _call("ns_experts_combine_backward", y.device, dout.data_ptr(), y.data_ptr(), slots.data_ptr(), _ptr(weights),
+    _call("ns_experts_combine_backward", y, dout.data_ptr(), y.data_ptr(), slots.data_ptr(), _ptr(weights),
           dy.data_ptr(), _ptr(dweights), tokens, top_k, n_rows, cols, _code(y.dtype))
     return dy, dweights
