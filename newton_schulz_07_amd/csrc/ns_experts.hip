@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "ns_device.h"
+#include "ns_lanes.h"
 #include "ns_sublayer.h"
 
 namespace ns {
@@ -546,7 +547,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const CombineGrad
     if (g.dweights) {
 #pragma unroll
       for (int u = 0; u < kCombineAhead; ++u) {
-        const float s = wave_sum(dot[u]);
+        const float s = lanes_sum<64>(dot[u]);
         if (lane == 0 && j0 + u < g.top_k) g.dweights[t * g.top_k + j0 + u] = slot[u] >= 0 ? s : 0.0f;
       }
     }

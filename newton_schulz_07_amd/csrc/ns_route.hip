@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "ns_device.h"
+#include "ns_lanes.h"
 #include "ns_sublayer.h"
 
 namespace ns {
@@ -55,39 +56,6 @@ template <typename T, int V> inline bool whole_vectors(const void* p, long long 
 // each other stays off the LDS) or 64, of V experts each; lane l of them
 // holds experts l V .. l V + V - 1.  16 lanes: four tokens share a wave's
 // instructions, which is what bounds a long batch.
-template <int R> __device__ __forceinline__ float ror(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + R, 0xf, 0xf, false));
-}
-template <int R> __device__ __forceinline__ int ror(int v) {
-  return __builtin_amdgcn_update_dpp(0, v, 0x120 + R, 0xf, 0xf, false);
-}
-template <int R> __device__ __forceinline__ double ror(double v) {
-  return __hiloint2double(ror<R>(__double2hiint(v)), ror<R>(__double2loint(v)));
-}
-template <int L, typename F, typename OP>
-__device__ __forceinline__ F over_lanes(F v, OP op) {
-  v = op(v, ror<8>(v));
-  v = op(v, ror<4>(v));
-  v = op(v, ror<2>(v));
-  v = op(v, ror<1>(v));
-  if (L == 64) {
-    v = op(v, __shfl_xor(v, 16, 64));
-    v = op(v, __shfl_xor(v, 32, 64));
-  }
-  return v;
-}
-__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }  // the other one of a NaN
-__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
-__device__ __forceinline__ int larger(int a, int b) { return max(a, b); }
-template <int L, typename F> __device__ __forceinline__ F lanes_max(F v) {
-  return over_lanes<L>(v, [](F a, F b) { return larger(a, b); });
-}
-template <int L> __device__ __forceinline__ int lanes_min(int v) {
-  return over_lanes<L>(v, [](int a, int b) { return a < b ? a : b; });
-}
-template <int L, typename F> __device__ __forceinline__ F lanes_sum(F v) {
-  return over_lanes<L>(v, [](F a, F b) { return a + b; });
-}
 __device__ __forceinline__ float inverse(float v) { return __builtin_amdgcn_rcpf(v); }  // within a step of 1 / v
 __device__ __forceinline__ double inverse(double v) { return 1.0 / v; }
 // exp(v) within 2 steps, 0 below 2^-126: 2^(v log2 e), with what the product's

@@ -184,7 +184,7 @@ int ns_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t 
     if (int s = check_arch()) return s;
     hipStream_t st = static_cast<hipStream_t>(stream);
     const int blocks = norm_backward_blocks(rows, (int)cols);
-    const size_t bytes = params ? (size_t)blocks * 2 * cols * sizeof(float) : 0;
+    const size_t bytes = params ? (size_t)blocks * 2 * partials_ld((int)cols) * sizeof(float) : 0;
     char* ws = nullptr;
     if (bytes > 0) {
       if (int s = get_workspace(st, bytes, &ws)) return s;

@@ -50,6 +50,8 @@ inline NormShape norm_shape(int cols) {
          : nv <= 4096 ? NormShape{1024, 4}
                       : NormShape{1024, 0};
 }
+// columns of a row of partial sums: whole vectors
+NS_HD constexpr int partials_ld(int cols) { return (cols + 7) / 8 * 8; }
 constexpr int kNormForwardBlocks = 2048, kNormBackwardBlocks = 512;
 inline long long norm_blocks(long long rows, NormShape s, long long most) {
   const long long need = s.tpr == 64 ? (rows + 3) / 4 : rows;
@@ -59,7 +61,7 @@ inline long long norm_blocks(long long rows, NormShape s, long long most) {
 // so long rows get fewer (at most 256 MiB of partials).
 inline int norm_backward_blocks(long long rows, int cols) {
   long long most = kNormBackwardBlocks;
-  const long long fit = (1ll << 28) / (8ll * cols);
+  const long long fit = (1ll << 28) / (8ll * partials_ld(cols));
   if (most > fit) most = fit > 0 ? fit : 1;
   return (int)norm_blocks(rows, norm_shape(cols), most);
 }
