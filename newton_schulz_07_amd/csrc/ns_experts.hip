@@ -17,6 +17,7 @@
 // The experts' row counts are known on the device only.  The grid holds the
 // most tiles that n_rows rows can make; every workgroup adds up the experts'
 // tiles (one prefix sum by each wave) and takes its own, or ends.
+#include <algorithm>
 #include <type_traits>
 
 #include "ns_device.h"
@@ -212,24 +213,27 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   }
 
   // Weight gradient: a load covers 64 / RC k rows of a stage, lane l the one
-  // of number l / RC, at a column that repeats every NC loads (nat_swz sees
-  // the last two bits of the k row in bf16, the last three in fp32).
+  // of number l / RC, at a column that repeats with the bits of the k row that
+  // nat_swz sees: every NCP (NCQ) loads.
   // Columns past the end read the last ones: what they add up to is never
   // stored.  k rows past the end must be zero: the descriptor ends there, or
   // the gathered row's offset is out of range.
   constexpr int RPP = 64 / RCP, RPQ = 64 / RCQ, KRQ = NQ * RPQ;
   const unsigned ldp = (unsigned)(g.fan_out * ES), ldq = (unsigned)(g.ldx * ES);
   const bool gather = WG && g.rows != nullptr;
-  constexpr int NC = ES == 2 ? 2 : 4;
-  static_assert(!WG || (NP % NC == 0 && NQ % NC == 0 && NC * RPP % (2 * NC) == 0 && NC * RPQ % (2 * NC) == 0),
-                "columns repeat every NC loads");
-  unsigned colp[WG ? NC : 1], colq[WG ? NC : 1];
+  constexpr int SEENP = ES == 4 ? 8 : RCP % 16 == 0 ? 4 : 16, SEENQ = ES == 4 ? 8 : RCQ % 16 == 0 ? 4 : 16;
+  constexpr int NCP = SEENP > RPP ? SEENP / RPP : 1, NCQ = SEENQ > RPQ ? SEENQ / RPQ : 1;
+  static_assert(!WG || (NP % NCP == 0 && NQ % NCQ == 0), "a wave's first k row starts a period");
+  static_assert(!QNAT || (ES == 4 ? RCQ >= 16 : RCQ >= 8), "nat_swz stays within a row");
+  static_assert(!PNAT || (ES == 4 ? RCP >= 16 : RCP >= 8), "nat_swz stays within a row");
+  unsigned colp[WG ? NCP : 1], colq[WG ? NCQ : 1];
   if constexpr (WG) {
 #pragma unroll
-    for (int t = 0; t < NC; ++t) {
+    for (int t = 0; t < NCP; ++t)
       colp[t] = (unsigned)(min(i0 + src(t).row, M - EPC) * ES) + (unsigned)(lane / RCP) * ldp;
+#pragma unroll
+    for (int t = 0; t < NCQ; ++t)
       colq[t] = (unsigned)(min(j0 + src(NP + t).row, N - EPC) * ES) + (gather ? 0u : (unsigned)(lane / RCQ) * ldq);
-    }
   }
   // x's row numbers of a wave's loads, read one stage ahead; past the expert's rows: none
   int idx[WG ? KRQ : 1];
@@ -257,7 +261,7 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
 #pragma unroll
       for (int t = 0; t < NIW; ++t) {
         if (t < NP) {
-          dma16(lds_of(slot, t), colp[t % NC] + (unsigned)(wave * NP + t) * RPP * ldp, p);
+          dma16(lds_of(slot, t), colp[t % NCP] + (unsigned)(wave * NP + t) * RPP * ldp, p);
           continue;
         }
         const int u = t - NP;
@@ -273,7 +277,7 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
         } else {
           o = (unsigned)(wave * NQ + u) * RPQ * ldq;
         }
-        dma16(lds_of(slot, t), o + colq[u % NC], q);
+        dma16(lds_of(slot, t), o + colq[u % NCQ], q);
       }
       read_idx(kt + 1);
     } else {
@@ -428,68 +432,96 @@ hipError_t launch_tiles(const ExpertsArgs& g, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Tiles of a launch: BM, BN, waves, 16-byte chunks of k, stages, workgroups
+// per CU.
 #define NS_EXPERTS_WIDE 256, 256, 2, 4, 8, 2, 1
 #define NS_EXPERTS_LONG 128, 256, 2, 2, 4, 3, 2
-#define NS_EXPERTS_F32 128, 128, 2, 2, 8, 3, 1
+#define NS_EXPERTS_SMALL 64, 64, 2, 2, 8, 3, 3
+#define NS_EXPERTS_FEW 32, 64, 1, 2, 8, 4, 3
+enum ExpertsTile { TILE_WIDE, TILE_LONG, TILE_SMALL, TILE_FEW };
 
-// Rows enough to fill 256-row tiles: an expert's last tile is half empty on
-// average.
-bool wide_tiles(ExpertsMode mode, const ExpertsArgs& g) {
-  return mode == EXP_PRODUCT && g.n_rows / g.experts >= 256;
+// The most tiles of bm x bn that a launch can have.
+long long most_tiles(ExpertsMode mode, const ExpertsArgs& g, int bm, int bn) {
+  if (mode == EXP_WEIGHT_GRAD)
+    return (long long)g.experts * ((g.fan_out + bm - 1) / bm) * ((g.fan_in + bn - 1) / bn);
+  const int n = mode == EXP_PRODUCT ? g.fan_out : g.fan_in;
+  return ((long long)g.n_rows / bm + std::min(g.experts, g.n_rows)) * ((n + bn - 1) / bn);
+}
+
+ExpertsTile choose_tile(int dtype, ExpertsMode mode, const ExpertsArgs& g) {
+  const int rows = g.n_rows / g.experts;  // an expert's, on average
+  const bool few = mode != EXP_WEIGHT_GRAD && rows <= 16;
+  if (dtype != 1) return few ? TILE_FEW : TILE_SMALL;
+  if (mode == EXP_PRODUCT && rows >= 256) return TILE_WIDE;
+  if (mode == EXP_PRODUCT && few) return TILE_FEW;
+  if (most_tiles(mode, g, 128, 256) >= 192) return TILE_LONG;
+  return few ? TILE_FEW : TILE_SMALL;
+}
+
+template <typename T, ExpertsMode MODE>
+hipError_t launch_type(const ExpertsArgs& g, hipStream_t st) {
+  constexpr bool BF16 = std::is_same<T, bf16>::value;
+  switch (choose_tile(BF16 ? 1 : 0, MODE, g)) {
+    case TILE_WIDE:
+      if constexpr (BF16 && MODE == EXP_PRODUCT) return launch_tiles<T, NS_EXPERTS_WIDE, MODE>(g, st);
+      break;
+    case TILE_LONG:
+      if constexpr (BF16) return launch_tiles<T, NS_EXPERTS_LONG, MODE>(g, st);
+      break;
+    case TILE_FEW:
+      if constexpr (MODE != EXP_WEIGHT_GRAD) return launch_tiles<T, NS_EXPERTS_FEW, MODE>(g, st);
+      break;
+    case TILE_SMALL: return launch_tiles<T, NS_EXPERTS_SMALL, MODE>(g, st);
+  }
+  return hipErrorInvalidValue;
 }
 
 template <ExpertsMode MODE>
 hipError_t launch_mode(int dtype, const ExpertsArgs& g, hipStream_t st) {
-  if (dtype != 1) return launch_tiles<float, NS_EXPERTS_F32, MODE>(g, st);
-  if constexpr (MODE == EXP_PRODUCT)
-    if (wide_tiles(MODE, g)) return launch_tiles<bf16, NS_EXPERTS_WIDE, MODE>(g, st);
-  return launch_tiles<bf16, NS_EXPERTS_LONG, MODE>(g, st);
+  return dtype == 1 ? launch_type<bf16, MODE>(g, st) : launch_type<float, MODE>(g, st);
 }
 
 // ---------------------------------------------------------------- combine
 
-// out[t] = sum_j weights[t, j] y[slots[t, j]]: a thread to 8 columns of a
-// token; eight rows are on their way before the first is added.
+// out[t] = sum_j weights[t, j] y[slots[t, j]]: TPT threads to a token, each
+// walking its columns 8 at a time; eight rows are on their way before the
+// first is added.
 constexpr int kCombineAhead = 8;
-template <typename T>
+template <typename T, int TPT>
 __global__ __launch_bounds__(256) void combine_kernel(const CombineArgs g) {
   const int vpr = g.cols / 8;
-  long long t;
-  int v;
-  if (vpr >= 256) {
-    t = blockIdx.x;
-    v = blockIdx.y * 256 + threadIdx.x;
-  } else {
-    const int tpb = 256 / vpr, tl = threadIdx.x / vpr;
-    t = (long long)blockIdx.x * tpb + tl;
-    v = threadIdx.x - tl * vpr;
-    if (tl >= tpb) return;
-  }
-  if (t >= g.tokens || v >= vpr) return;
+  const long long t = (long long)blockIdx.x * (256 / TPT) + threadIdx.x / TPT;
+  if (t >= g.tokens) return;
   const Raw8<T>* y = reinterpret_cast<const Raw8<T>*>(g.y);
-  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int j0 = 0; j0 < g.top_k; j0 += kCombineAhead) {
-    Raw8<T> r[kCombineAhead];
-    float w[kCombineAhead];
+  for (int v = blockIdx.y * TPT + threadIdx.x % TPT; v < vpr; v += gridDim.y * TPT) {
+    float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int j0 = 0; j0 < g.top_k; j0 += kCombineAhead) {
+      Raw8<T> r[kCombineAhead];
+      float w[kCombineAhead];
+      int slot[kCombineAhead];
 #pragma unroll
-    for (int u = 0; u < kCombineAhead; ++u) {
-      r[u] = Raw8<T>{};
-      w[u] = 0.0f;
-      if (j0 + u >= g.top_k) continue;
-      const int slot = g.slots[t * g.top_k + j0 + u];
-      if ((unsigned)slot >= (unsigned)g.n_rows) continue;
-      w[u] = g.weights ? g.weights[t * g.top_k + j0 + u] : 1.0f;
-      r[u] = y[(size_t)slot * vpr + v];
+      for (int u = 0; u < kCombineAhead; ++u) {
+        const int j = min(j0 + u, g.top_k - 1);
+        slot[u] = g.slots[t * g.top_k + j];
+        w[u] = g.weights ? g.weights[t * g.top_k + j] : 1.0f;
+        if (j0 + u >= g.top_k || (unsigned)slot[u] >= (unsigned)g.n_rows) slot[u] = -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kCombineAhead; ++u) {
+        r[u] = Raw8<T>{};
+        if (slot[u] >= 0) r[u] = y[(size_t)slot[u] * vpr + v];
+        else w[u] = 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < kCombineAhead; ++u) {
+        float f[8];
+        unpack8(r[u], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = fmaf(w[u], f[e], s[e]);
+      }
     }
-#pragma unroll
-    for (int u = 0; u < kCombineAhead; ++u) {
-      float f[8];
-      unpack8(r[u], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] = fmaf(w[u], f[e], s[e]);
-    }
+    reinterpret_cast<Raw8<T>*>(g.out)[(size_t)t * vpr + v] = pack8(s, T());
   }
-  reinterpret_cast<Raw8<T>*>(g.out)[(size_t)t * vpr + v] = pack8(s, T());
 }
 
 // dy[slot] = weight dout[t],  dweights[t, j] = <dout[t], y[slot]>: a wave to a
@@ -566,8 +598,12 @@ hipError_t launch_experts(int dtype, ExpertsMode mode, const ExpertsArgs& g, hip
 
 const char* experts_config(int dtype, ExpertsMode mode, const ExpertsArgs& g) {
 #define NS_TEXT(NAME, TILE) NAME ": dtype=%s rows=%lld experts=%lld fan_out=%lld fan_in=%lld | tile=" TILE
-#define NS_TILES(NAME)                                                                               \
-  dtype != 1 ? NS_TEXT(NAME, "128x128") : wide_tiles(mode, g) ? NS_TEXT(NAME, "256x256") : NS_TEXT(NAME, "128x256")
+#define NS_TILES(NAME)                                  \
+  tile == TILE_WIDE    ? NS_TEXT(NAME, "256x256")       \
+  : tile == TILE_SMALL ? NS_TEXT(NAME, "64x64")         \
+  : tile == TILE_FEW   ? NS_TEXT(NAME, "32x64")         \
+                       : NS_TEXT(NAME, "128x256")
+  const ExpertsTile tile = choose_tile(dtype, mode, g);
   return mode == EXP_PRODUCT      ? (NS_TILES("experts product"))
          : mode == EXP_INPUT_GRAD ? (NS_TILES("experts input gradient"))
                                   : (NS_TILES("experts weight gradient"));
@@ -575,11 +611,17 @@ const char* experts_config(int dtype, ExpertsMode mode, const ExpertsArgs& g) {
 #undef NS_TEXT
 }
 
+template <int TPT>
+static void launch_combine_of(int dtype, const CombineArgs& g, int pieces, hipStream_t st) {
+  const dim3 grid((unsigned)((g.tokens + 256 / TPT - 1) / (256 / TPT)), (unsigned)pieces);
+  if (dtype == 1) dispatch(combine_kernel<bf16, TPT>, grid, dim3(256), st, g);
+  else dispatch(combine_kernel<float, TPT>, grid, dim3(256), st, g);
+}
 hipError_t launch_combine(int dtype, const CombineArgs& g, hipStream_t st) {
-  const int vpr = g.cols / 8, tpb = vpr >= 256 ? 1 : 256 / vpr;
-  const dim3 grid((unsigned)((g.tokens + tpb - 1) / tpb), (unsigned)(vpr >= 256 ? (vpr + 255) / 256 : 1));
-  if (dtype == 1) dispatch(combine_kernel<bf16>, grid, dim3(256), st, g);
-  else dispatch(combine_kernel<float>, grid, dim3(256), st, g);
+  const int vpr = g.cols / 8;
+  if (vpr > 64) launch_combine_of<256>(dtype, g, (vpr + 255) / 256, st);
+  else if (vpr > 16) launch_combine_of<64>(dtype, g, 1, st);
+  else launch_combine_of<16>(dtype, g, 1, st);
   return hipGetLastError();
 }
 
