@@ -408,7 +408,7 @@ int ns_route_backward(const void* logits, int64_t ld, const int32_t* ids,
  *
  *   x         [n_x, fan_in] dtype, rows ldx elements apart (a multiple of 8);
  *             read through rows it must hold less than 2 GiB.
- *   rows      int32 [n_rows], or NULL: sorted row i is row i of x.  A row
+ *   rows      int32 [n_rows], fewer than 2^29, or NULL: sorted row i is row i of x.  A row
  *             number outside [0, n_x) reads as zeros.
  *   w         [experts, fan_out, fan_in] dtype.
  *   offsets   int32 [experts + 1] on the device, ascending from 0 to n_rows;

@@ -126,6 +126,14 @@ __device__ __forceinline__ void dma16(unsigned lds_byte_addr, unsigned voff, i32
                : "memory", "m0");
 }
 
+// The same, 4 bytes per lane at m0 + 4 * lane.
+__device__ __forceinline__ void dma4(unsigned lds_byte_addr, unsigned voff, i32x4 rsrc) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :
+               : "s"(lds_byte_addr), "v"(voff), "s"(rsrc)
+               : "memory", "m0");
+}
+
 __device__ __forceinline__ unsigned lds_addr(const uint4* p) {
   return (unsigned)reinterpret_cast<unsigned long long>((__attribute__((address_space(3))) const uint4*)p);
 }

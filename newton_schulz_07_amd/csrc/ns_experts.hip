@@ -115,8 +115,6 @@ __device__ __forceinline__ i32x4 uniform(i32x4 r) {
   return u;
 }
 
-typedef const __attribute__((address_space(4))) int* ConstInts;  // read with scalar loads
-
 template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, int MODE>
 __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_kernel(const ExpertsArgs g) {
   constexpr bool PNAT = MODE == EXP_WEIGHT_GRAD, QNAT = MODE != EXP_PRODUCT;
@@ -131,6 +129,7 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   static_assert(LP % (64 * NW) == 0 && LQ % (64 * NW) == 0, "operands must split into whole wave loads");
   static_assert(ST >= 2 && NIW * (ST - 2) < 64, "ring depth");
   __shared__ uint4 lds[lds_chunks(BM, BN, CPR, ST, ES)];
+  __shared__ int row_ring[MODE == EXP_WEIGHT_GRAD ? ST * NW * 64 : 1];  // see read_rows
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -214,10 +213,10 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
 
   // Weight gradient: a load covers 64 / RC k rows of a stage, lane l the one
   // of number l / RC, at a column that repeats with the bits of the k row that
-  // nat_swz sees: every NCP (NCQ) loads.
-  // Columns past the end read the last ones: what they add up to is never
-  // stored.  k rows past the end must be zero: the descriptor ends there, or
-  // the gathered row's offset is out of range.
+  // nat_swz sees: every NCP (NCQ) loads.  Columns past the end read the last
+  // ones: what they add up to is never stored.  k rows past the end must be
+  // zero: the descriptor ends there, or the gathered row's offset is out of
+  // range.
   constexpr int RPP = 64 / RCP, RPQ = 64 / RCQ, KRQ = NQ * RPQ;
   const unsigned ldp = (unsigned)(g.fan_out * ES), ldq = (unsigned)(g.ldx * ES);
   const bool gather = WG && g.rows != nullptr;
@@ -235,19 +234,19 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
     for (int t = 0; t < NCQ; ++t)
       colq[t] = (unsigned)(min(j0 + src(NP + t).row, N - EPC) * ES) + (gather ? 0u : (unsigned)(lane / RCQ) * ldq);
   }
-  // x's row numbers of a wave's loads, read one stage ahead; past the expert's rows: none
-  int idx[WG ? KRQ : 1];
-  const ConstInts rows_c = (ConstInts)(unsigned long long)(g.rows + (g.rows ? tl.begin : 0));
-  auto read_idx = [&](int kt) __attribute__((always_inline)) {
-    if constexpr (WG) {
-      if (!gather || kt * BK >= K) return;
-      const int k = kt * BK + wave * KRQ;
-#pragma unroll
-      for (int r = 0; r < KRQ; ++r) {
-        const int v = rows_c[min(k + r, K - 1)];
-        idx[r] = k + r < K ? v : -1;
-      }
-    }
+  // x's row numbers: a wave keeps those of its own loads in the LDS, the KRQ of
+  // stage kt at row_ring[kt % ST][wave].  They go out ST - 1 stages before the
+  // loads that they are for, as one more load of that stage (LD in all), and
+  // have landed when those are issued: the wave has waited for its loads of
+  // stage kt - (ST - 1) by then.  (Scalar loads would return out of order with
+  // the fragment reads, each of which would wait for all of them.)
+  constexpr int LD = NIW + (WG ? 1 : 0);
+  static_assert(!WG || KRQ <= 64, "one load holds a wave's row numbers");
+  const i32x4 rR = WG && gather ? uniform(make_rsrc(g.rows + tl.begin, (unsigned)K * 4u)) : i32x4{};
+  auto read_rows = [&](int kt, int slot) __attribute__((always_inline)) {
+    if constexpr (WG)
+      dma4(lds_addr(reinterpret_cast<const uint4*>(row_ring + (slot * NW + wave) * 64)),
+           (unsigned)(kt * BK + wave * KRQ + lane) * 4u, rR);  // past the expert's rows: zeros
   };
 
   auto issue = [&](int kt, int slot) __attribute__((always_inline)) {
@@ -264,22 +263,17 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
           dma16(lds_of(slot, t), colp[t % NCP] + (unsigned)(wave * NP + t) * RPP * ldp, p);
           continue;
         }
-        const int u = t - NP;
+        const int u = t - NP, kr = wave * KRQ + u * RPQ + lane / RCQ;
         unsigned o;
         if (gather) {
-          // row offsets in scalars; a lane takes that of its k row
-          auto at = [&](int r) __attribute__((always_inline)) -> unsigned {
-            return (unsigned)idx[r] < (unsigned)g.n_x ? (unsigned)idx[r] * ldq : kOutOfRange;
-          };
-          o = at(u * RPQ);
-#pragma unroll
-          for (int v = 1; v < RPQ; ++v) o = lane / RCQ == v ? at(u * RPQ + v) : o;
+          const int r = row_ring[(slot * NW + wave) * 64 + u * RPQ + lane / RCQ];
+          o = k0 + kr < K && (unsigned)r < (unsigned)g.n_x ? (unsigned)r * ldq : kOutOfRange;
         } else {
           o = (unsigned)(wave * NQ + u) * RPQ * ldq;
         }
         dma16(lds_of(slot, t), o + colq[u % NCQ], q);
       }
-      read_idx(kt + 1);
+      if (gather) read_rows(kt + ST - 1, (slot + ST - 1) % ST);
     } else {
       const bool whole = k0 + BK <= K;
 #pragma unroll
@@ -345,10 +339,15 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   uint4 pf[2][SM], qf[2][SN];
   auto wait_stage = [&](int kt) __attribute__((always_inline)) {
     const int later = nk - 1 - kt;  // stages that may be in flight after kt, at most ST - 2
-    if (later >= ST - 2) wait_vm_lgkm0<NIW * (ST - 2)>();
-    else if (ST > 4 && later == 2) wait_vm_lgkm0<NIW * 2>();
-    else if (ST > 3 && later == 1) wait_vm_lgkm0<NIW * 1>();
-    else wait_vm_lgkm0<0>();
+    if (WG && !gather) {  // (NIW loads to a stage)
+      if (later >= ST - 2) wait_vm_lgkm0<NIW * (ST - 2)>();
+      else wait_vm_lgkm0<0>();
+    } else {
+      if (later >= ST - 2) wait_vm_lgkm0<LD * (ST - 2)>();
+      else if (ST > 4 && later == 2) wait_vm_lgkm0<LD * 2>();
+      else if (ST > 3 && later == 1) wait_vm_lgkm0<LD * 1>();
+      else wait_vm_lgkm0<0>();
+    }
     ring_barrier();
   };
   static_assert(ST <= 5 && KS % 2 == 0, "tail waits; fragment buffers alternate");
@@ -369,7 +368,12 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
         for (int b = 0; b < SN; ++b) mfma_chunk(acc[a][b], qf[s & 1][b], pf[s & 1][a], T());
     }
   };
-  read_idx(0);
+  if (WG && gather && nk > 0) {
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s) read_rows(s, s);
+    wait_vm_lgkm0<0>();
+    asm volatile("" ::: "memory");
+  }
 #pragma unroll
   for (int s = 0; s < ST - 1; ++s)
     if (s < nk) issue(s, s);

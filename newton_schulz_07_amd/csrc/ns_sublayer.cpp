@@ -107,6 +107,8 @@ int check_x(const void* x, int64_t ldx, int64_t n_x, const void* rows, int64_t n
   if (rows == nullptr && n_x < n_rows) return fail(NS_ERR_INVALID_ARG, "x has fewer rows than n_rows");
   if (rows != nullptr && span(n_x, ldx, fan_in, elem_size(dtype)) > (size_t(1) << 31) - 16)
     return fail(NS_ERR_INVALID_ARG, "x read through rows must hold less than 2 GiB");
+  if (rows != nullptr && n_rows >= (int64_t(1) << 29))
+    return fail(NS_ERR_INVALID_ARG, "rows must hold fewer than 2^29 row numbers (2 GiB)");
   return NS_OK;
 }
 
