@@ -81,33 +81,6 @@ __device__ __forceinline__ Tile find_tile(const ExpertsArgs& g, int bm, int upto
   return t;
 }
 
-// Weight gradient: workgroup w -> expert and tile q of its T tiles.  Experts
-// differ in their rows and so in the time of their tiles; each XCD (w mod 8)
-// therefore takes about an eighth of the tiles of EVERY expert, the remainder
-// of T / 8 dealt out so that it has T tiles of every 8 experts.  (With one
-// contiguous range of tiles for each XCD the one with the largest experts
-// ends last.)
-__device__ __forceinline__ int expert_tile(int w, int experts, int T, int* q) {
-  const int x = w % 8, octet = w / 8 / T;
-  if (octet < experts / 8) {
-    int m = w / 8 - octet * T, o = 0;
-    for (int i = 0;; ++i) {
-      const int p = T / 8 + (((x - o + 8) % 8) < T % 8 ? 1 : 0);
-      if (m < p || i == 7) {
-        int before = 0;  // XCDs below x that take one more tile of this expert
-        for (int y = 0; y < x; ++y) before += ((y - o + 8) % 8) < T % 8 ? 1 : 0;
-        *q = x * (T / 8) + before + m;
-        return octet * 8 + i;
-      }
-      m -= p;
-      o = (o + T % 8) % 8;
-    }
-  }
-  const int e0 = experts / 8 * 8, lin = xcd_remap(w - e0 * T, (experts - e0) * T);
-  *q = lin % T;
-  return e0 + lin / T;
-}
-
 // The descriptor, in scalar registers (it is the same in every lane).
 __device__ __forceinline__ i32x4 uniform(i32x4 r) {
   i32x4 u = {__builtin_amdgcn_readfirstlane(r[0]), __builtin_amdgcn_readfirstlane(r[1]),
@@ -142,17 +115,20 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   Tile tl;
   int i0, j0;
   if (MODE == EXP_WEIGHT_GRAD) {
-    const int tiles_m = (M + BM - 1) / BM, per = tiles_m * tiles_n;
-    int q, ti, tj;
-    const int e = expert_tile(blockIdx.x, g.experts, per, &q);
-    rect_decode(q, tiles_m, tiles_n, ti, tj);
-    tl.expert = e;
-    tl.tile = ti;
-    expert_rows(g.offsets, e, g.experts, g.n_rows, &tl.begin, &tl.count);
+    // The grid is [experts][tiles].  Workgroups go to the XCDs in turn, so each
+    // XCD has an eighth of the tiles of every expert (experts differ in their
+    // rows and so in the time of their tiles); with a multiple of 8 tiles it is
+    // a run of neighbours, which share their columns of x.
+    const int tiles_m = (M + BM - 1) / BM, tiles = gridDim.x, w = blockIdx.x;
+    const int q = tiles % 8 == 0 ? w % 8 * (tiles / 8) + w / 8 : w;
+    tl.expert = blockIdx.y;
+    int tj;
+    rect_decode(q, tiles_m, tiles_n, tl.tile, tj);
+    i0 = tl.tile * BM;
+    j0 = tj * BN;
+    expert_rows(g.offsets, tl.expert, g.experts, g.n_rows, &tl.begin, &tl.count);
     tl.begin = __builtin_amdgcn_readfirstlane(tl.begin);
     tl.count = __builtin_amdgcn_readfirstlane(tl.count);
-    i0 = ti * BM;
-    j0 = tj * BN;
   } else {
     int upto;
     const int total = count_tiles(g, BM, &upto) * tiles_n;
@@ -249,7 +225,10 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
            (unsigned)(kt * BK + wave * KRQ + lane) * 4u, rR);  // past the expert's rows: zeros
   };
 
-  auto issue = [&](int kt, int slot) __attribute__((always_inline)) {
+  typedef std::integral_constant<int, 3> Both;
+  // what: 1 P's loads, 2 Q's, 3 both
+  auto issue = [&](int kt, int slot, auto what) __attribute__((always_inline)) {
+    constexpr bool DOP = decltype(what)::value & 1, DOQ = decltype(what)::value & 2;
     const int k0 = kt * BK;
     if constexpr (WG) {
       const unsigned left = (unsigned)min(BK, K - k0);  // > 0
@@ -259,6 +238,7 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
       const i32x4 q = uniform(make_rsrc(x, (gather ? (unsigned)g.n_x - 1 : left - 1) * ldq + (unsigned)(g.fan_in * ES)));
 #pragma unroll
       for (int t = 0; t < NIW; ++t) {
+        if (t < NP ? !DOP : !DOQ) continue;
         if (t < NP) {
           dma16(lds_of(slot, t), colp[t % NCP] + (unsigned)(wave * NP + t) * RPP * ldp, p);
           continue;
@@ -273,11 +253,12 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
         }
         dma16(lds_of(slot, t), o + colq[u % NCQ], q);
       }
-      if (gather) read_rows(kt + ST - 1, (slot + ST - 1) % ST);
+      if (DOQ && gather) read_rows(kt + ST - 1, (slot + ST - 1) % ST);
     } else {
       const bool whole = k0 + BK <= K;
 #pragma unroll
       for (int t = 0; t < NIW; ++t) {
+        if (t < NP ? !DOP : !DOQ) continue;
         // (an offset out of range stays there: kt steps are below 2^31)
         const unsigned o = off[t] + (unsigned)kt * (t < NP ? (unsigned)(BK * ES) : step_q);
         dma16(lds_of(slot, t), whole || k0 + src(t).kpos < K ? o : kOutOfRange, t < NP ? rP : rQ);
@@ -352,7 +333,7 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   };
   static_assert(ST <= 5 && KS % 2 == 0, "tail waits; fragment buffers alternate");
   auto stage = [&](int kt, int u) __attribute__((always_inline)) {
-    if (kt + ST - 1 < nk) issue(kt + ST - 1, (u + ST - 1) % ST);
+    if (kt + ST - 1 < nk) issue(kt + ST - 1, (u + ST - 1) % ST, Both());
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       if (s + 1 < KS) {
@@ -368,15 +349,29 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
         for (int b = 0; b < SN; ++b) mfma_chunk(acc[a][b], qf[s & 1][b], pf[s & 1][a], T());
     }
   };
-  if (WG && gather && nk > 0) {
+  if (WG && gather) {
+    // P's first loads do not wait for the row numbers
+    if (nk > 0) {
 #pragma unroll
-    for (int s = 0; s < ST - 1; ++s) read_rows(s, s);
-    wait_vm_lgkm0<0>();
-    asm volatile("" ::: "memory");
+      for (int s = 0; s < ST - 1; ++s) read_rows(s, s);
+#pragma unroll
+      for (int s = 0; s < ST - 1; ++s)
+        if (s < nk) issue(s, s, std::integral_constant<int, 1>());
+      if (nk >= ST - 1) wait_vm_lgkm0<NP * (ST - 1)>();
+      else wait_vm_lgkm0<0>();
+      asm volatile("" ::: "memory");
+    }
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s)
+      if (s < nk) issue(s, s, std::integral_constant<int, 2>());
+    static_assert(!WG || ST <= 3, "the first wait");
+    if (nk > 1) wait_vm_lgkm0<(NQ + 1) * (ST - 2)>();  // Q's loads of stage 1
+    else wait_vm_lgkm0<0>();
+  } else {
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s)
+      if (s < nk) issue(s, s, Both());
   }
-#pragma unroll
-  for (int s = 0; s < ST - 1; ++s)
-    if (s < nk) issue(s, s);
   if (nk > 0) {
     wait_stage(0);
     load_step(0, 0, pf[0], qf[0]);
@@ -421,9 +416,10 @@ template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, 
 hipError_t launch_tiles(const ExpertsArgs& g, hipStream_t st) {
   const int N = MODE == EXP_PRODUCT ? g.fan_out : g.fan_in;
   const long long tiles_n = (N + BN - 1) / BN;
-  long long grid;
+  long long grid, experts = 1;
   if (MODE == EXP_WEIGHT_GRAD) {
-    grid = (long long)g.experts * ((g.fan_out + BM - 1) / BM) * tiles_n;
+    grid = (g.fan_out + BM - 1) / BM * tiles_n;
+    experts = g.experts;
   } else {
     // sum of ceil(c / BM) over at most min(experts, n_rows) non-empty experts
     const long long some = g.experts < g.n_rows ? g.experts : g.n_rows;
@@ -432,14 +428,14 @@ hipError_t launch_tiles(const ExpertsArgs& g, hipStream_t st) {
   }
   if (grid <= 0) return hipSuccess;
   if (grid > 0x7fffffffll) return hipErrorInvalidValue;
-  dispatch(experts_kernel<T, BM, BN, WM, WN, CPR, ST, OCC, MODE>, dim3((unsigned)grid), dim3(WM * WN * 64), st, g);
+  dispatch(experts_kernel<T, BM, BN, WM, WN, CPR, ST, OCC, MODE>, dim3((unsigned)grid, (unsigned)experts), dim3(WM * WN * 64), st, g);
   return hipGetLastError();
 }
 
 // Tiles of a launch: BM, BN, waves, 16-byte chunks of k, stages, workgroups
 // per CU.
 #define NS_EXPERTS_WIDE 256, 256, 2, 4, 8, 2, 1
-#define NS_EXPERTS_LONG 128, 256, 2, 2, 4, 3, 2
+#define NS_EXPERTS_LONG 128, 256, 2, 4, 4, 3, 2
 #define NS_EXPERTS_SMALL 64, 64, 2, 2, 8, 3, 3
 #define NS_EXPERTS_FEW 32, 64, 1, 2, 8, 4, 3
 enum ExpertsTile { TILE_WIDE, TILE_LONG, TILE_SMALL, TILE_FEW };
