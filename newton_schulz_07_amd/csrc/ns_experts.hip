@@ -81,6 +81,13 @@ __device__ __forceinline__ Tile find_tile(const ExpertsArgs& g, int bm, int upto
   return t;
 }
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f32x4 acc_of(const f32x16& v, int rg) {  // 4 columns of a 32 x 32 block's row
+  return f32x4{v[4 * rg], v[4 * rg + 1], v[4 * rg + 2], v[4 * rg + 3]};
+}
+// bf16 pairs of 4 columns
+__device__ __forceinline__ uint2 pack4(f32x4 v) { return make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])); }
+
 // The descriptor, in scalar registers (it is the same in every lane).
 __device__ __forceinline__ i32x4 uniform(i32x4 r) {
   i32x4 u = {__builtin_amdgcn_readfirstlane(r[0]), __builtin_amdgcn_readfirstlane(r[1]),
@@ -96,13 +103,15 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   constexpr int WTM = BM / WM, WTN = BN / WN, SM = WTM / 32, SN = WTN / 32;
   constexpr int LP = BM * CPR, LQ = BN * CPR, STAGE = LP + LQ;
   constexpr int NP = LP / 64 / NW, NQ = LQ / 64 / NW, NIW = NP + NQ;  // a wave's loads of a stage
-  constexpr int ERC = epi_row_chunks(BN, ES);
+  constexpr int OCH = WTN / EPC, OPITCH = OCH + 1;  // chunks of a wave's output row, and of its place in the LDS
+  constexpr int OUT = NW * 32 * OPITCH;             // 32 such rows for each wave
+  constexpr bool WG = MODE == EXP_WEIGHT_GRAD;
   constexpr int RCP = BM / EPC, RCQ = BN / EPC;
   static_assert(WTM % 32 == 0 && WTN % 32 == 0, "wave tile must be whole 32x32 blocks");
   static_assert(LP % (64 * NW) == 0 && LQ % (64 * NW) == 0, "operands must split into whole wave loads");
   static_assert(ST >= 2 && NIW * (ST - 2) < 64, "ring depth");
-  __shared__ uint4 lds[lds_chunks(BM, BN, CPR, ST, ES)];
-  __shared__ int row_ring[MODE == EXP_WEIGHT_GRAD ? ST * NW * 64 : 1];  // see read_rows
+  __shared__ uint4 lds[ST * STAGE > OUT ? ST * STAGE : OUT];  // the ring, then the output
+  __shared__ int row_ring[WG ? ST * NW * 64 : 1];  // see read_rows
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -155,7 +164,6 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
 
   // Product and input gradient: byte offsets at k0 = 0, kOutOfRange for rows
   // and columns past the end, and one descriptor for each operand.
-  constexpr bool WG = MODE == EXP_WEIGHT_GRAD;
   unsigned off[WG ? 1 : NIW];
   const unsigned step_q = (unsigned)((QNAT ? BK * g.fan_in : BK) * ES);
   i32x4 rP{}, rQ{};
@@ -222,7 +230,7 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   auto read_rows = [&](int kt, int slot) __attribute__((always_inline)) {
     if constexpr (WG)
       dma4(lds_addr(reinterpret_cast<const uint4*>(row_ring + (slot * NW + wave) * 64)),
-           (unsigned)(kt * BK + wave * KRQ + lane) * 4u, rR);  // past the expert's rows: zeros
+           (unsigned)(kt * BK + wave * KRQ + lane) * 4u, rR);  // past the expert's rows: zeros (not used)
   };
 
   typedef std::integral_constant<int, 3> Both;
@@ -350,8 +358,7 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
     }
   };
   if (WG && gather) {
-    // P's first loads do not wait for the row numbers
-    if (nk > 0) {
+    if (nk > 0) {  // P's first loads do not wait for the row numbers
 #pragma unroll
       for (int s = 0; s < ST - 1; ++s) read_rows(s, s);
 #pragma unroll
@@ -384,31 +391,42 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
 #pragma unroll
   for (int u = 0; u < ST - 1; ++u)
     if (kt0 + u < nk) stage(kt0 + u, u);
-  wait_vm_lgkm0<0>();
+  wait_vm_lgkm0<0>();  // (row numbers that nothing asked for may still be on their way)
   __syncthreads();
 
-  // the tile through LDS to whole 16-byte stores
-  T* O = reinterpret_cast<T*>(g.out) +
-         (MODE == EXP_WEIGHT_GRAD ? (size_t)tl.expert * g.fan_out * g.fan_in : (size_t)tl.begin * N);
-  T* S = reinterpret_cast<T*>(lds);
-  constexpr int SROW = ERC * EPC;
+  // 32 rows of a wave's output at a time, through its place in the LDS to whole
+  // rows of 16-byte stores.  (bf16: two lanes' four columns make one lane's
+  // eight, so the LDS is written 16 bytes at a time too.)
+  T* O = reinterpret_cast<T*>(g.out) + (WG ? (size_t)tl.expert * g.fan_out * g.fan_in : (size_t)tl.begin * N);
+  uint4* const mine = lds + wave * 32 * OPITCH;
 #pragma unroll
-  for (int a = 0; a < SM; ++a)
+  for (int a = 0; a < SM; ++a) {
 #pragma unroll
-    for (int b = 0; b < SN; ++b)
+    for (int b = 0; b < SN; ++b) {
+      if constexpr (ES == 2) {
 #pragma unroll
-      for (int rg = 0; rg < 4; ++rg) {
-        const float v[4] = {acc[a][b][4 * rg], acc[a][b][4 * rg + 1], acc[a][b][4 * rg + 2], acc[a][b][4 * rg + 3]};
-        *reinterpret_cast<typename Quad<T>::Raw*>(S + (wm * WTM + a * 32 + acc_i(lane)) * SROW + wn * WTN + b * 32 +
-                                                  acc_j(rg, lane)) = Quad<T>::pack(v);
+        for (int rg = 0; rg < 4; rg += 2) {
+          const uint2 x = pack4(acc_of(acc[a][b], rg)), y = pack4(acc_of(acc[a][b], rg + 1));
+          const auto p = __builtin_amdgcn_permlane32_swap(x.x, y.x, false, false);
+          const auto q = __builtin_amdgcn_permlane32_swap(x.y, y.y, false, false);
+          mine[acc_i(lane) * OPITCH + b * 4 + rg + (lane >> 5)] = make_uint4(p[0], q[0], p[1], q[1]);
+        }
+      } else {
+#pragma unroll
+        for (int rg = 0; rg < 4; ++rg)
+          mine[acc_i(lane) * OPITCH + b * 8 + acc_j(rg, lane) / 4] =
+              __builtin_bit_cast(uint4, acc_of(acc[a][b], rg));
       }
-  __syncthreads();
-  constexpr int CPT = BN / EPC;
-  for (int qd = tid; qd < BM * CPT; qd += NT) {
-    const int il = qd / CPT, c = qd % CPT;
-    const int i = i0 + il, j = j0 + c * EPC;
-    if (i >= m_end || j >= N) continue;
-    *reinterpret_cast<uint4*>(O + (size_t)i * N + j) = *reinterpret_cast<const uint4*>(S + il * SROW + c * EPC);
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int c0 = 0; c0 < 32 * OCH; c0 += 64) {
+      const int r = (c0 + lane) / OCH, c = (c0 + lane) % OCH;
+      const int i = i0 + wm * WTM + a * 32 + r, j = j0 + wn * WTN + c * EPC;
+      const uint4 v = mine[r * OPITCH + c];
+      if (i < m_end && j < N) *reinterpret_cast<uint4*>(O + (size_t)i * N + j) = v;
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -435,6 +453,7 @@ hipError_t launch_tiles(const ExpertsArgs& g, hipStream_t st) {
 // Tiles of a launch: BM, BN, waves, 16-byte chunks of k, stages, workgroups
 // per CU.
 #define NS_EXPERTS_WIDE 256, 256, 2, 4, 8, 2, 1
+#define NS_EXPERTS_WIDE_GRAD 256, 256, 2, 4, 4, 3, 1
 #define NS_EXPERTS_LONG 128, 256, 2, 4, 4, 3, 2
 #define NS_EXPERTS_SMALL 64, 64, 2, 2, 8, 3, 3
 #define NS_EXPERTS_FEW 32, 64, 1, 2, 8, 4, 3
@@ -453,6 +472,7 @@ ExpertsTile choose_tile(int dtype, ExpertsMode mode, const ExpertsArgs& g) {
   const bool few = mode != EXP_WEIGHT_GRAD && rows <= 16;
   if (dtype != 1) return few ? TILE_FEW : TILE_SMALL;
   if (mode == EXP_PRODUCT && rows >= 256) return TILE_WIDE;
+  if (mode == EXP_WEIGHT_GRAD && most_tiles(mode, g, 256, 256) >= 768) return TILE_WIDE;
   if (mode == EXP_PRODUCT && few) return TILE_FEW;
   if (most_tiles(mode, g, 128, 256) >= 192) return TILE_LONG;
   return few ? TILE_FEW : TILE_SMALL;
@@ -464,6 +484,7 @@ hipError_t launch_type(const ExpertsArgs& g, hipStream_t st) {
   switch (choose_tile(BF16 ? 1 : 0, MODE, g)) {
     case TILE_WIDE:
       if constexpr (BF16 && MODE == EXP_PRODUCT) return launch_tiles<T, NS_EXPERTS_WIDE, MODE>(g, st);
+      if constexpr (BF16 && MODE == EXP_WEIGHT_GRAD) return launch_tiles<T, NS_EXPERTS_WIDE_GRAD, MODE>(g, st);
       break;
     case TILE_LONG:
       if constexpr (BF16) return launch_tiles<T, NS_EXPERTS_LONG, MODE>(g, st);

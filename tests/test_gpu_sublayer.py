@@ -372,6 +372,42 @@ def test_experts_products(dtype, case, gather):
                   max(counts), dtype)
 
 
+def some_rows(experts, most, seed):
+    return np.random.default_rng(seed).integers(0, most + 1, experts).tolist()
+
+
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("counts,N,K,tiles", [
+    # the larger tiles, ragged in rows and columns, with experts of no row, one and several stages
+    (some_rows(100, 60, 1), 264, 520, ("128x256", "128x256", "128x256")),
+    (some_rows(200, 100, 2) + [0, 0, 1, 31, 32, 33, 64, 65], 520, 264, ("128x256", "128x256", "256x256")),
+    (some_rows(52, 700, 3), 1032, 776, ("256x256", "128x256", "256x256")),
+    ([300, 0, 513], 1288, 2056, ("256x256", "64x64", "128x256")),
+])
+def test_experts_large_tiles(counts, N, K, tiles, gather):
+    dtype, dev = torch.bfloat16, device()
+    M, E = sum(counts), len(counts)
+    n_x = M // 2 if gather else M
+    offsets, rows = routed(counts, n_x, 180)
+    rows = rows if gather else None
+    x, w, dy = normal((n_x, K), 181, dtype), normal((E, N, K), 182, dtype), normal((M, N), 183, dtype)
+    to = lambda t: None if t is None else t.to(dev)  # noqa: E731
+    R, O = None if rows is None else rows.numpy(), offsets.numpy()
+    X, W, D = to64(x), to64(w), to64(dy)
+    xg, wg, dyg, og, rg = to(x), to(w), to(dy), to(offsets), to(rows)
+    y = ns.ns_experts_product(xg, wg, og, rg)
+    assert "tile=" + tiles[0] in ns.ns_query_last_config()
+    products_near(y, ref.experts_product(X, W, O, R), ref.experts_product(abs(X), abs(W), O, R), K, dtype)
+    dx = ns.ns_experts_input_grad(dyg, wg, og)
+    assert "tile=" + tiles[1] in ns.ns_query_last_config()
+    products_near(dx, ref.experts_input_grad(D, W, O), ref.experts_input_grad(abs(D), abs(W), O), N, dtype)
+    want, mag = ref.experts_weight_grad(D, X, O, R), ref.experts_weight_grad(abs(D), abs(X), O, R)
+    for _ in range(3):
+        dw = ns.ns_experts_weight_grad(dyg, xg, og, rg)
+        assert "tile=" + tiles[2] in ns.ns_query_last_config()
+        products_near(dw, want, mag, max(counts), dtype)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_experts_rows_apart_and_repeats(dtype):
     # x as rows of a wider matrix; the same bits on every call
