@@ -381,6 +381,7 @@ void launch_forward(const LayerNormArgs& g, hipStream_t st) {
   NS_LN(64, 4);
   NS_LN(256, 2);
   NS_LN(256, 4);
+  NS_LN(1024, 2);
   NS_LN(1024, 4);
 #undef NS_LN
   dispatch(layer_norm_long_kernel<T, HOW>, grid, block, st, g);
@@ -397,6 +398,7 @@ void launch_backward(const LayerNormGradArgs& g, int blocks, hipStream_t st) {
   NS_LN(64, 4);
   NS_LN(256, 2);
   NS_LN(256, 4);
+  NS_LN(1024, 2);
   NS_LN(1024, 4);
 #undef NS_LN
   dispatch(layer_norm_backward_long_kernel<T, HOW>, grid, block, st, g);

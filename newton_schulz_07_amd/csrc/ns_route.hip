@@ -603,7 +603,7 @@ __device__ __forceinline__ void place_tokens(const RouteArgs& g, int p0, int p1,
 // plan too.  More: a block takes kRouteWaves 64 / L tokens and leaves its
 // experts' counts in hist[block].
 template <typename T, int L, int V, bool WIDE, bool SINGLE>
-__global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(const RouteArgs g) {
+__global__ __launch_bounds__((SINGLE ? kRouteSingleWaves : kRouteWaves) * 64) void route_kernel(const RouteArgs g) {
   constexpr int TPW = 64 / L;
   extern __shared__ char smem[];
   int* hist = reinterpret_cast<int*>(smem);  // [experts]
@@ -806,7 +806,7 @@ void launch_v(RouteArgs g, hipStream_t st) {
   g.vec = whole_vectors<T, V>(g.logits, g.ld, g.experts);
   g.vec_bias = whole_vectors<float, V>(g.bias, 0, g.experts);
   const RouteShape r = route_shape(g.tokens, g.experts);
-  const int waves = r.blocks == 1 ? std::min(kRouteWaves, (g.tokens + r.tokens_per_wave - 1) / r.tokens_per_wave) : kRouteWaves;
+  const int waves = r.blocks == 1 ? std::min(kRouteSingleWaves, (g.tokens + r.tokens_per_wave - 1) / r.tokens_per_wave) : kRouteWaves;
   const bool wide = g.bias != nullptr || g.groups > 1;
   const size_t keys = waves * route_keys_bytes(r.tokens_per_wave, g.experts, g.groups);
   const size_t cnt = r.blocks == 1 ? (size_t)waves * g.experts * 2 : 0;

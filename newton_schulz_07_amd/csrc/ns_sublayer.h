@@ -47,6 +47,7 @@ inline NormShape norm_shape(int cols) {
          : nv <= 256  ? NormShape{64, 4}
          : nv <= 512  ? NormShape{256, 2}
          : nv <= 1024 ? NormShape{256, 4}
+         : nv <= 2048 ? NormShape{1024, 2}
          : nv <= 4096 ? NormShape{1024, 4}
                       : NormShape{1024, 0};
 }
@@ -74,7 +75,8 @@ hipError_t launch_layer_norm_backward(int dtype, const LayerNormGradArgs& g, int
 
 constexpr int kMaxExperts = 1024, kMaxTopK = 64, kMaxGroups = 64;
 constexpr int kRouteWaves = 16;        // waves of a routing block, at most
-constexpr int kRouteSingleTokens = 64;  // up to here one block does it all
+constexpr int kRouteSingleTokens = 64;  // up to here one block does it all,
+constexpr int kRouteSingleWaves = 8;    // of so many waves (more would spill registers)
 constexpr int kRouteUnscannedBlocks = 256;
 
 struct RouteArgs {
