@@ -18,6 +18,7 @@
 // decide stand closer than that can tell apart, it is chosen for again in 64
 // bits.  Logits without a bias are compared as they are.
 #include <algorithm>
+#include <type_traits>
 
 #include "ns_device.h"
 #include "ns_lanes.h"
@@ -603,7 +604,7 @@ __device__ __forceinline__ void place_tokens(const RouteArgs& g, int p0, int p1,
 // plan too.  More: a block takes kRouteWaves 64 / L tokens and leaves its
 // experts' counts in hist[block].
 template <typename T, int L, int V, bool WIDE, bool SINGLE>
-__global__ __launch_bounds__((SINGLE ? kRouteSingleWaves : kRouteWaves) * 64) void route_kernel(const RouteArgs g) {
+__global__ __launch_bounds__((SINGLE ? route_single_waves(L * V) : kRouteWaves) * 64) void route_kernel(const RouteArgs g) {
   constexpr int TPW = 64 / L;
   extern __shared__ char smem[];
   int* hist = reinterpret_cast<int*>(smem);  // [experts]
@@ -732,12 +733,13 @@ __global__ __launch_bounds__(1024) void route_place_kernel(const RouteArgs g, in
   place_tokens(g, t0 * g.top_k, t1 * g.top_k, base, cnt);
 }
 
-// dlogits of a token by L lanes.  With p_j = s_j / (sum + 1e-20), or s_j:
+// dlogits of a token by one wave.  With p_j = s_j / (sum + 1e-20), or s_j:
 //   ds_j = scale (dw_j - sum_i dw_i p_i) / (sum + 1e-20), or scale dw_j
 //   sigmoid: dl_e = ds_e s_e (1 - s_e);  softmax: dl_e = s_e (ds_e - sum_j ds_j s_j)
 // dw is spread over the experts in LDS; NaN there: not chosen.
-template <typename T, int L, int V>
+template <typename T, int V>
 __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs g) {
+  constexpr int L = 64;
   extern __shared__ float spread[];  // [tokens of the block][experts]
   const int ll = threadIdx.x & (L - 1), E = g.experts, e0 = ll * V;
   const int t = blockIdx.x * (256 / L) + threadIdx.x / L;
@@ -806,61 +808,54 @@ void launch_v(RouteArgs g, hipStream_t st) {
   g.vec = whole_vectors<T, V>(g.logits, g.ld, g.experts);
   g.vec_bias = whole_vectors<float, V>(g.bias, 0, g.experts);
   const RouteShape r = route_shape(g.tokens, g.experts);
-  const int waves = r.blocks == 1 ? std::min(kRouteSingleWaves, (g.tokens + r.tokens_per_wave - 1) / r.tokens_per_wave) : kRouteWaves;
-  const bool wide = g.bias != nullptr || g.groups > 1;
-  const size_t keys = waves * route_keys_bytes(r.tokens_per_wave, g.experts, g.groups);
-  const size_t cnt = r.blocks == 1 ? (size_t)waves * g.experts * 2 : 0;
+  const bool wide = g.bias != nullptr || g.groups > 1, single = r.blocks == 1;
+  const size_t keys = r.waves * route_keys_bytes(r.tokens_per_wave, g.experts, g.groups);
+  const size_t cnt = single ? (size_t)r.waves * g.experts * 2 : 0;
   const size_t lds = route_lds_ints(g.experts) + (keys > cnt ? keys : cnt);  // at most 144 KiB, with 1024 experts in groups
-  const dim3 grid(r.blocks), block(std::max(waves, 1) * 64);
-  if (r.blocks == 1) {
-    if (wide) dispatch_lds(route_kernel<T, L, V, true, true>, grid, block, lds, st, g);
-    else dispatch_lds(route_kernel<T, L, V, false, true>, grid, block, lds, st, g);
-  } else {
+  const dim3 grid(r.blocks), block(r.waves * 64);
+  if (!single) {
     if (wide) dispatch_lds(route_kernel<T, L, V, true, false>, grid, block, lds, st, g);
     else dispatch_lds(route_kernel<T, L, V, false, false>, grid, block, lds, st, g);
+  } else if constexpr (L == 64) {  // (few tokens: a wave to each)
+    if (wide) dispatch_lds(route_kernel<T, L, V, true, true>, grid, block, lds, st, g);
+    else dispatch_lds(route_kernel<T, L, V, false, true>, grid, block, lds, st, g);
   }
 }
 
-template <typename T>
-void launch_t(const RouteArgs& g, hipStream_t st) {
-  if (g.experts <= 16) launch_v<T, 16, 1>(g, st);
-  else if (g.experts <= 32) launch_v<T, 16, 2>(g, st);
-  else if (g.experts <= 64) launch_v<T, 16, 4>(g, st);
-  else if (g.experts <= 128) launch_v<T, 16, 8>(g, st);
-  else if (g.experts <= 256) launch_v<T, 16, 16>(g, st);
-  else if (g.experts <= 512) launch_v<T, 64, 8>(g, st);
-  else launch_v<T, 64, 16>(g, st);
-}
-
-template <typename T, int L, int V>
+template <typename T, int V>
 void launch_grad_v(RouteGradArgs g, hipStream_t st) {
   g.vec = whole_vectors<T, V>(g.logits, g.ld, g.experts);
   g.vec_out = whole_vectors<T, V>(g.dlogits, g.experts, g.experts);
-  const int tb = 256 / L;
-  dispatch_lds(route_backward_kernel<T, L, V>, dim3((g.tokens + tb - 1) / tb), dim3(256), (size_t)tb * g.experts * 8, st,
+  constexpr int tb = 4;
+  dispatch_lds(route_backward_kernel<T, V>, dim3((g.tokens + tb - 1) / tb), dim3(256), (size_t)tb * g.experts * 8, st,
                g);
 }
 
-template <typename T>
-void launch_grad(const RouteGradArgs& g, hipStream_t st) {
-  if (g.experts <= 16) launch_grad_v<T, 16, 1>(g, st);
-  else if (g.experts <= 32) launch_grad_v<T, 16, 2>(g, st);
-  else if (g.experts <= 64) launch_grad_v<T, 16, 4>(g, st);
-  else if (g.experts <= 128) launch_grad_v<T, 16, 8>(g, st);
-  else if (g.experts <= 256) launch_grad_v<T, 16, 16>(g, st);
-  else if (g.experts <= 512) launch_grad_v<T, 64, 8>(g, st);
-  else launch_grad_v<T, 64, 16>(g, st);
+// Calls f with the experts of a lane, of L lanes.
+template <int L, typename F>
+void for_width(int experts, F f) {
+  if (experts <= L) f(std::integral_constant<int, 1>());
+  else if (experts <= 2 * L) f(std::integral_constant<int, 2>());
+  else if (experts <= 4 * L) f(std::integral_constant<int, 4>());
+  else if (experts <= 8 * L) f(std::integral_constant<int, 8>());
+  else f(std::integral_constant<int, 16>());
 }
 
 }  // namespace
 
 hipError_t launch_route(int dtype, const RouteArgs& g, hipStream_t st) {
-  if (dtype == 1) launch_t<bf16>(g, st);
-  else launch_t<float>(g, st);
-  if (hipError_t e = hipGetLastError()) return e;
   const RouteShape r = route_shape(g.tokens, g.experts);
+  auto lanes = [&](auto l) {
+    for_width<l.value>(g.experts, [&](auto v) {
+      if (dtype == 1) launch_v<bf16, l.value, v.value>(g, st);
+      else launch_v<float, l.value, v.value>(g, st);
+    });
+  };
+  if (r.tokens_per_wave == 4) lanes(std::integral_constant<int, 16>());
+  else lanes(std::integral_constant<int, 64>());
+  if (hipError_t e = hipGetLastError()) return e;
   if (g.offsets == nullptr || r.blocks == 1) return hipSuccess;
-  const int block_tokens = kRouteWaves * r.tokens_per_wave;
+  const int block_tokens = r.waves * r.tokens_per_wave;
   // Reading every block's counts costs each block time that grows with their
   // number; a scan costs a launch.  At 256 blocks of 128 experts the blocks
   // read 128 KiB each.
@@ -880,8 +875,10 @@ hipError_t launch_route(int dtype, const RouteArgs& g, hipStream_t st) {
 }
 
 hipError_t launch_route_backward(int dtype, const RouteGradArgs& g, hipStream_t st) {
-  if (dtype == 1) launch_grad<bf16>(g, st);
-  else launch_grad<float>(g, st);
+  for_width<64>(g.experts, [&](auto v) {
+    if (dtype == 1) launch_grad_v<bf16, v.value>(g, st);
+    else launch_grad_v<float, v.value>(g, st);
+  });
   return hipGetLastError();
 }
 

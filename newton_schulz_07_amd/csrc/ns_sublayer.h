@@ -53,7 +53,7 @@ inline NormShape norm_shape(int cols) {
 }
 // columns of a row of partial sums: whole vectors
 NS_HD constexpr int partials_ld(int cols) { return (cols + 7) / 8 * 8; }
-constexpr int kNormForwardBlocks = 2048, kNormBackwardBlocks = 512;
+constexpr int kNormForwardBlocks = 2048, kNormBackwardBlocks = 512, kNormLongBackwardBlocks = 256;
 inline long long norm_blocks(long long rows, NormShape s, long long most) {
   const long long need = s.tpr == 64 ? (rows + 3) / 4 : rows;
   return need < most ? need : most;
@@ -61,10 +61,11 @@ inline long long norm_blocks(long long rows, NormShape s, long long most) {
 // Blocks of the backward pass: each has 8 bytes of partial sums per column,
 // so long rows get fewer (at most 256 MiB of partials).
 inline int norm_backward_blocks(long long rows, int cols) {
-  long long most = kNormBackwardBlocks;
+  const NormShape s = norm_shape(cols);
+  long long most = s.tpr == 1024 ? kNormLongBackwardBlocks : kNormBackwardBlocks;
   const long long fit = (1ll << 28) / (8ll * partials_ld(cols));
   if (most > fit) most = fit > 0 ? fit : 1;
-  return (int)norm_blocks(rows, norm_shape(cols), most);
+  return (int)norm_blocks(rows, s, most);
 }
 
 hipError_t launch_layer_norm(int dtype, const LayerNormArgs& g, hipStream_t st);
@@ -74,10 +75,10 @@ hipError_t launch_layer_norm_backward(int dtype, const LayerNormGradArgs& g, int
 // --------------------------------------------------------------- routing
 
 constexpr int kMaxExperts = 1024, kMaxTopK = 64, kMaxGroups = 64;
-constexpr int kRouteWaves = 16;        // waves of a routing block, at most
-constexpr int kRouteSingleTokens = 64;  // up to here one block does it all,
-constexpr int kRouteSingleWaves = 8;    // of so many waves (more would spill registers)
+constexpr int kRouteLeastWaves = 8, kRouteWaves = 16;  // waves of a routing block, where it is not the only one
 constexpr int kRouteUnscannedBlocks = 256;
+// of the one block that few tokens take (with more than 256 experts 16 would spill registers)
+constexpr int route_single_waves(int experts) { return experts > 256 ? kRouteWaves / 2 : kRouteWaves; }
 
 struct RouteArgs {
   const void* logits;  // [tokens, experts], rows ld elements apart
@@ -101,13 +102,25 @@ struct RouteGradArgs {
   float scale;
   bool vec, vec_out;
 };
-// A token takes 16 lanes of a wave up to 256 experts, then all 64.
+static_assert(route_single_waves(kMaxExperts) >= kRouteLeastWaves, "tokens for more than one block make more than one");
+// A token takes a whole wave, or 16 lanes where the tokens fill the card and
+// there are at most 256 experts.  A block has few waves as long as there are
+// at most kRouteUnscannedBlocks of them.
 struct RouteShape {
-  int tokens_per_wave, blocks, hist_ld;
+  int tokens_per_wave, waves, blocks, hist_ld;
 };
 inline RouteShape route_shape(int tokens, int experts) {
-  const int tpw = experts <= 256 ? 4 : 1, tb = kRouteWaves * tpw;
-  return RouteShape{tpw, tokens <= kRouteSingleTokens ? 1 : (int)(((long long)tokens + tb - 1) / tb), (experts + 3) / 4 * 4};
+  RouteShape r{1, route_single_waves(experts), 1, (experts + 3) / 4 * 4};
+  if (tokens <= r.waves) {
+    if (tokens > 0) r.waves = tokens;
+    return r;
+  }
+  if (experts <= 256 && tokens > kRouteWaves * kRouteUnscannedBlocks) r.tokens_per_wave = 4;
+  for (r.waves = kRouteLeastWaves;; r.waves *= 2) {
+    const int tb = r.waves * r.tokens_per_wave;
+    r.blocks = (int)(((long long)tokens + tb - 1) / tb);
+    if (r.blocks <= kRouteUnscannedBlocks || r.waves == kRouteWaves) return r;
+  }
 }
 inline size_t route_workspace(int tokens, int experts) {
   const RouteShape r = route_shape(tokens, experts);
