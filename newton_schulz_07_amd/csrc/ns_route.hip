@@ -369,10 +369,12 @@ __device__ __forceinline__ bool choose(const RouteArgs& g, const T* row, long lo
 #pragma unroll
         for (int v = 0; v < V; ++v) sum += l[v] == -INFINITY ? 0.0 : exp((double)l[v] - (double)top);
         sum = lanes_sum<L>(sum);
+        if (top == -INFINITY && !nan) sum = 1.0;  // nothing but -inf: scores of zero
       }
       if (ll < n) {
         const double x = logit(row, LOW - (mine[0] & LOW));
-        exact = (softmax ? exp(x - (double)top) / sum : 1.0 / (1.0 + exp(-x))) + (double)g.bias[LOW - (mine[0] & LOW)];
+        exact = softmax ? (x == -INFINITY ? 0.0 : exp(x - (double)top)) / sum : 1.0 / (1.0 + exp(-x));
+        exact += (double)g.bias[LOW - (mine[0] & LOW)];
       }
     } else if (ll < n) {
       exact = logit(row, LOW - (mine[0] & LOW));

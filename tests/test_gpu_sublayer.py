@@ -207,6 +207,55 @@ def test_route_many_tokens():
     check_route(logits, (5,), {}, ns.ns_route(logits.to(device()), 5))
 
 
+# longer than 4096 tokens: a token takes 16 lanes, of 1 to 16 experts each, or 64; blocks with and without a scan
+LONG_ROUTES = [
+    (4097, 7, 7, 1, 1, 2), (4500, 24, 4, 24, 5, 2), (4200, 64, 6, 8, 4, 2), (9000, 100, 8, 1, 1, 2),
+    (4100, 256, 8, 8, 3, 2), (16500, 20, 17, 1, 1, 2), (4200, 300, 5, 4, 2, 1),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", LONG_ROUTES)
+def test_route_long_batches(dtype, case):
+    T, E, k, G, tg, gb = case
+    logits = normal((T, E), 68 + E, dtype, 1.5)
+    dev = device()
+    for bias, score in ((None, "softmax"), (normal((E,), 69, scale=0.1), "sigmoid")):
+        kw = dict(groups=G, top_groups=tg, group_best=gb, score=score)
+        r = ns.ns_route(logits.to(dev), k, bias=None if bias is None else bias.to(dev), **kw)
+        check_route(logits, (k,), dict(kw, bias=None if bias is None else to64(bias)), r)
+
+
+@pytest.mark.parametrize("experts", [12, 80, 250, 600])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("groups", [1, 2])
+def test_route_edge_rows_choose_alike_in_short_and_long_batches(experts, bias, groups):
+    # equal and nearly equal keys, masked, infinite and NaN logits; twice, as a repair of close keys must not
+    # hang on the order of anything
+    nan, inf, E = float("nan"), float("inf"), experts
+    rows = torch.round(normal((24, E), 71) * 2) / 2
+    rows[1] = 0.0
+    rows[2, 5:] = -inf
+    rows[3] = -inf
+    rows[4, 7] = nan
+    rows[5, 3:] = nan
+    rows[6, 9] = inf
+    rows[7, 4:10] = inf
+    rows[8:12] = normal((4, E), 72, scale=1e-4)
+    rows[12:16] = 1.0 + torch.arange(E) % 3 * 2.0 ** -23
+    b = torch.round(normal((E,), 73) * 4) / 64 if bias else None
+    dev = device()
+    kw = dict(groups=groups, top_groups=1, group_best=1)
+    want = ref.route(to64(rows), 6, bias=to64(b) if bias else None, **kw)[0]
+    for n in (10, 24, 24 * 172, 24 * 700):
+        logits = rows.repeat(max(1, n // 24), 1)[:n].to(dev)
+        for _ in range(2):
+            r = ns.ns_route(logits, 6, bias=b.to(dev) if bias else None, **kw)
+            got = r.ids.cpu().numpy()
+            assert np.array_equal(got, np.tile(want, (max(1, n // 24), 1))[:n]), n
+            assert np.array_equal(r.rows[r.slots.long()].cpu().numpy(), np.arange(n)[:, None].repeat(6, 1))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_ties_go_to_the_lower_index(score):
     logits = torch.zeros(70, 96)
