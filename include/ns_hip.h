@@ -316,7 +316,8 @@ int ns_stage_update(const void* x, const void* c_off, const float* c_diag,
  *     contiguous.  Index, offset and fp32 vectors need 4-byte alignment only.
  *   - Outputs share no memory with inputs or with each other
  *     (NS_ERR_INVALID_ARG).
- *   - A dimension of a row is at most 2^20, a row count below 2^31.
+ *   - A row's length, and the elements between rows, are at most 2^20, a row
+ *     count below 2^31.
  *   - Sums are taken in fp32 and every result is rounded once to its type.
  *     No atomics touch a floating-point value: the same inputs give the same
  *     bits.
@@ -380,7 +381,7 @@ enum {
  *             sorted row i holds token rows[i] (int32 [tokens * top_k]);
  *             choice j of token t is sorted row slots[t, j] (int32).
  *
- * experts <= 1024, top_k <= 64, groups <= 64 and a divisor of experts.
+ * tokens < 2^25, experts <= 1024, top_k <= 64, groups <= 64 and a divisor of experts.
  * Keys that pass through exp are compared in 64 bits.  A logit of -inf has
  * score 0 and comes last; a row of nothing else has weights 0.  A NaN key
  * counts as -inf, a NaN score makes the weights it enters NaN; ids are always
@@ -408,8 +409,8 @@ int ns_route_backward(const void* logits, int64_t ld, const int32_t* ids,
  *
  *   x         [n_x, fan_in] dtype, rows ldx elements apart (a multiple of 8);
  *             read through rows it must hold less than 2 GiB.
- *   rows      int32 [n_rows], fewer than 2^29, or NULL: sorted row i is row i of x.  A row
- *             number outside [0, n_x) reads as zeros.
+ *   rows      int32 [n_rows], fewer than 2^29, or NULL: sorted row i is row i
+ *             of x.  A row number outside [0, n_x) reads as zeros.
  *   w         [experts, fan_out, fan_in] dtype.
  *   offsets   int32 [experts + 1] on the device, ascending from 0 to n_rows;
  *             values are clamped to [0, n_rows], and rows of y that no expert

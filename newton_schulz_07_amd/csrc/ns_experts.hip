@@ -508,40 +508,42 @@ hipError_t launch_mode(int dtype, const ExpertsArgs& g, hipStream_t st) {
 // walking its columns 8 at a time; eight rows are on their way before the
 // first is added.
 constexpr int kCombineAhead = 8;
+constexpr int kCombineBlocks = 1 << 20;  // a launch holds fewer than 2^32 threads: more tokens than that go round
 template <typename T, int TPT>
 __global__ __launch_bounds__(256) void combine_kernel(const CombineArgs g) {
   const int vpr = g.cols / 8;
-  const long long t = (long long)blockIdx.x * (256 / TPT) + threadIdx.x / TPT;
-  if (t >= g.tokens) return;
   const Raw8<T>* y = reinterpret_cast<const Raw8<T>*>(g.y);
-  for (int v = blockIdx.y * TPT + threadIdx.x % TPT; v < vpr; v += gridDim.y * TPT) {
-    float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int j0 = 0; j0 < g.top_k; j0 += kCombineAhead) {
-      Raw8<T> r[kCombineAhead];
-      float w[kCombineAhead];
-      int slot[kCombineAhead];
+  for (long long t = (long long)blockIdx.x * (256 / TPT) + threadIdx.x / TPT; t < g.tokens;
+       t += (long long)gridDim.x * (256 / TPT)) {
+    for (int v = blockIdx.y * TPT + threadIdx.x % TPT; v < vpr; v += gridDim.y * TPT) {
+      float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      for (int j0 = 0; j0 < g.top_k; j0 += kCombineAhead) {
+        Raw8<T> r[kCombineAhead];
+        float w[kCombineAhead];
+        int slot[kCombineAhead];
 #pragma unroll
-      for (int u = 0; u < kCombineAhead; ++u) {
-        const int j = min(j0 + u, g.top_k - 1);
-        slot[u] = g.slots[t * g.top_k + j];
-        w[u] = g.weights ? g.weights[t * g.top_k + j] : 1.0f;
-        if (j0 + u >= g.top_k || (unsigned)slot[u] >= (unsigned)g.n_rows) slot[u] = -1;
+        for (int u = 0; u < kCombineAhead; ++u) {
+          const int j = min(j0 + u, g.top_k - 1);
+          slot[u] = g.slots[t * g.top_k + j];
+          w[u] = g.weights ? g.weights[t * g.top_k + j] : 1.0f;
+          if (j0 + u >= g.top_k || (unsigned)slot[u] >= (unsigned)g.n_rows) slot[u] = -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kCombineAhead; ++u) {
+          r[u] = Raw8<T>{};
+          if (slot[u] >= 0) r[u] = y[(size_t)slot[u] * vpr + v];
+          else w[u] = 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kCombineAhead; ++u) {
+          float f[8];
+          unpack8(r[u], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] = fmaf(w[u], f[e], s[e]);
+        }
       }
-#pragma unroll
-      for (int u = 0; u < kCombineAhead; ++u) {
-        r[u] = Raw8<T>{};
-        if (slot[u] >= 0) r[u] = y[(size_t)slot[u] * vpr + v];
-        else w[u] = 0.0f;
-      }
-#pragma unroll
-      for (int u = 0; u < kCombineAhead; ++u) {
-        float f[8];
-        unpack8(r[u], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] = fmaf(w[u], f[e], s[e]);
-      }
+      reinterpret_cast<Raw8<T>*>(g.out)[(size_t)t * vpr + v] = pack8(s, T());
     }
-    reinterpret_cast<Raw8<T>*>(g.out)[(size_t)t * vpr + v] = pack8(s, T());
   }
 }
 
@@ -550,58 +552,58 @@ __global__ __launch_bounds__(256) void combine_kernel(const CombineArgs g) {
 template <typename T>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const CombineGradArgs g) {
   const int lane = threadIdx.x & 63, vpr = g.cols / 8;
-  const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= g.tokens) return;
   const Raw8<T>* y = reinterpret_cast<const Raw8<T>*>(g.y);
-  const Raw8<T>* dout = reinterpret_cast<const Raw8<T>*>(g.dout) + (size_t)t * vpr;
   Raw8<T>* dy = reinterpret_cast<Raw8<T>*>(g.dy);
-  for (int j0 = 0; j0 < g.top_k; j0 += kCombineAhead) {
-    int slot[kCombineAhead];
-    float w[kCombineAhead], dot[kCombineAhead];
-#pragma unroll
-    for (int u = 0; u < kCombineAhead; ++u) {
-      const bool on = j0 + u < g.top_k;
-      slot[u] = on ? g.slots[t * g.top_k + j0 + u] : -1;
-      if ((unsigned)slot[u] >= (unsigned)g.n_rows) slot[u] = -1;
-      w[u] = on && g.weights ? g.weights[t * g.top_k + j0 + u] : 1.0f;
-      dot[u] = 0.0f;
-    }
-    for (int v = lane; v < vpr; v += 64) {
-      float d[8];
-      unpack8(dout[v], d);
-      Raw8<T> r[kCombineAhead];
-      if (g.dweights) {
-#pragma unroll
-        for (int u = 0; u < kCombineAhead; ++u) {
-          r[u] = Raw8<T>{};
-          if (slot[u] >= 0) r[u] = y[(size_t)slot[u] * vpr + v];
-        }
-      }
-      if (dy) {
-#pragma unroll
-        for (int u = 0; u < kCombineAhead; ++u) {
-          if (slot[u] < 0) continue;
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = w[u] * d[e];
-          dy[(size_t)slot[u] * vpr + v] = pack8(f, T());
-        }
-      }
-      if (g.dweights) {
-#pragma unroll
-        for (int u = 0; u < kCombineAhead; ++u) {
-          float f[8];
-          unpack8(r[u], f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dot[u] = fmaf(f[e], d[e], dot[u]);
-        }
-      }
-    }
-    if (g.dweights) {
+  for (long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); t < g.tokens; t += (long long)gridDim.x * 4) {
+    const Raw8<T>* dout = reinterpret_cast<const Raw8<T>*>(g.dout) + (size_t)t * vpr;
+    for (int j0 = 0; j0 < g.top_k; j0 += kCombineAhead) {
+      int slot[kCombineAhead];
+      float w[kCombineAhead], dot[kCombineAhead];
 #pragma unroll
       for (int u = 0; u < kCombineAhead; ++u) {
-        const float s = lanes_sum<64>(dot[u]);
-        if (lane == 0 && j0 + u < g.top_k) g.dweights[t * g.top_k + j0 + u] = slot[u] >= 0 ? s : 0.0f;
+        const bool on = j0 + u < g.top_k;
+        slot[u] = on ? g.slots[t * g.top_k + j0 + u] : -1;
+        if ((unsigned)slot[u] >= (unsigned)g.n_rows) slot[u] = -1;
+        w[u] = on && g.weights ? g.weights[t * g.top_k + j0 + u] : 1.0f;
+        dot[u] = 0.0f;
+      }
+      for (int v = lane; v < vpr; v += 64) {
+        float d[8];
+        unpack8(dout[v], d);
+        Raw8<T> r[kCombineAhead];
+        if (g.dweights) {
+#pragma unroll
+          for (int u = 0; u < kCombineAhead; ++u) {
+            r[u] = Raw8<T>{};
+            if (slot[u] >= 0) r[u] = y[(size_t)slot[u] * vpr + v];
+          }
+        }
+        if (dy) {
+#pragma unroll
+          for (int u = 0; u < kCombineAhead; ++u) {
+            if (slot[u] < 0) continue;
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = w[u] * d[e];
+            dy[(size_t)slot[u] * vpr + v] = pack8(f, T());
+          }
+        }
+        if (g.dweights) {
+#pragma unroll
+          for (int u = 0; u < kCombineAhead; ++u) {
+            float f[8];
+            unpack8(r[u], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot[u] = fmaf(f[e], d[e], dot[u]);
+          }
+        }
+      }
+      if (g.dweights) {
+#pragma unroll
+        for (int u = 0; u < kCombineAhead; ++u) {
+          const float s = lanes_sum<64>(dot[u]);
+          if (lane == 0 && j0 + u < g.top_k) g.dweights[t * g.top_k + j0 + u] = slot[u] >= 0 ? s : 0.0f;
+        }
       }
     }
   }
@@ -634,7 +636,7 @@ const char* experts_config(int dtype, ExpertsMode mode, const ExpertsArgs& g) {
 
 template <int TPT>
 static void launch_combine_of(int dtype, const CombineArgs& g, int pieces, hipStream_t st) {
-  const dim3 grid((unsigned)((g.tokens + 256 / TPT - 1) / (256 / TPT)), (unsigned)pieces);
+  const dim3 grid((unsigned)std::min(kCombineBlocks, (g.tokens + 256 / TPT - 1) / (256 / TPT)), (unsigned)pieces);
   if (dtype == 1) dispatch(combine_kernel<bf16, TPT>, grid, dim3(256), st, g);
   else dispatch(combine_kernel<float, TPT>, grid, dim3(256), st, g);
 }
@@ -647,7 +649,7 @@ hipError_t launch_combine(int dtype, const CombineArgs& g, hipStream_t st) {
 }
 
 hipError_t launch_combine_backward(int dtype, const CombineGradArgs& g, hipStream_t st) {
-  const dim3 grid((unsigned)((g.tokens + 3) / 4));
+  const dim3 grid((unsigned)std::min(kCombineBlocks, (g.tokens + 3) / 4));
   if (dtype == 1) dispatch(combine_backward_kernel<bf16>, grid, dim3(256), st, g);
   else dispatch(combine_backward_kernel<float>, grid, dim3(256), st, g);
   return hipGetLastError();

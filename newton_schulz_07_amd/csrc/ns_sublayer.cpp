@@ -12,6 +12,7 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 20;     // columns of a row, and elements between rows
 constexpr int64_t kMaxRows = int64_t(1) << 31;    // row counts stay below
+constexpr int64_t kMaxTokens = int64_t(1) << 25;  // and routed tokens: a launch holds fewer than 2^32 threads, 64 to a token
 
 int check_rows(int64_t n, const char* name) {
   if (n < 0 || n >= kMaxRows) return fail(NS_ERR_INVALID_ARG, std::string(name) + " must be in [0, 2^31)");
@@ -70,12 +71,11 @@ const char* type_name(int dtype) { return dtype == NS_DTYPE_BF16 ? "bf16" : "fp3
 
 int check_route(int64_t tokens, int64_t experts, int64_t top_k, int64_t ld, int score, int dtype) {
   if (int s = check_dtype(dtype)) return s;
-  if (int s = check_rows(tokens, "tokens")) return s;
+  if (tokens < 0 || tokens >= kMaxTokens) return fail(NS_ERR_INVALID_ARG, "tokens must be in [0, 2^25)");
   if (experts < 1 || experts > kMaxExperts)
     return fail(NS_ERR_INVALID_ARG, "experts must be in [1, " + std::to_string(kMaxExperts) + "]");
   if (top_k < 1 || top_k > kMaxTopK || top_k > experts)
     return fail(NS_ERR_INVALID_ARG, "top_k must be in [1, min(experts, " + std::to_string(kMaxTopK) + ")]");
-  if (tokens * top_k >= kMaxRows) return fail(NS_ERR_INVALID_ARG, "tokens * top_k must be below 2^31");
   if (int s = check_ld(ld, experts, "ld")) return s;
   if (score != NS_SCORE_SOFTMAX && score != NS_SCORE_SIGMOID)
     return fail(NS_ERR_INVALID_ARG, "score must be NS_SCORE_SOFTMAX or NS_SCORE_SIGMOID");

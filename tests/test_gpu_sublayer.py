@@ -565,6 +565,24 @@ def test_combine(dtype, case, weighted):
         assert dw is None
 
 
+def test_combine_more_tokens_than_a_launch_holds_blocks():
+    # 2^24 + 5 tokens: output offsets past 2^32 elements, and blocks that go round
+    T, cols, dev = (1 << 24) + 5, 520, device()
+    y = normal((16, cols), 105, torch.bfloat16).to(dev)
+    slots = (torch.arange(T, device=dev, dtype=torch.int32) % 16).view(T, 1)
+    out = ns.ns_experts_combine(y, slots)
+    at = torch.cat([torch.arange(0, T, 65537), torch.arange(T - 40, T)]).to(dev)
+    assert torch.equal(out[at], y[at % 16])
+    w = torch.ones(T, 1, device=dev)
+    dw = torch.empty_like(w)
+    status = ns.lib().ns_experts_combine_backward(  # no dy: choices share rows of y
+        out.data_ptr(), y.data_ptr(), slots.data_ptr(), w.data_ptr(), None, dw.data_ptr(), T, 1, 16, cols,
+        ns.NS_DTYPE_BF16, torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    norms = (y.double() ** 2).sum(1)
+    near(dw[at, 0], to64(norms[at % 16]), to64(norms[at % 16]) * cols * U)
+
+
 def test_combine_bad_slots_add_nothing():
     dev = device()
     y, w = normal((12, 64), 104), normal((4, 3), 105)

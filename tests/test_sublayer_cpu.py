@@ -120,10 +120,11 @@ BIG = 1 << 31
             (dict(groups=7), 1), (dict(top_groups=9), 1), (dict(top_groups=0), 1),
             (dict(top_k=9, top_groups=1), 1), (dict(group_best=3), 1), (dict(score=2), 1), (dict(ld=63), 1),
             (dict(tokens=-1), 1), (dict(tokens=BIG // 4, top_k=4), 1), (dict(dtype=3), 2), (dict(ids=A), 1),
-            (dict(slots=D + 65536), 1)]),
+            (dict(slots=D + 65536), 1), (dict(tokens=1 << 25, top_k=1), 1)]),
         ("ns_route_backward", ROUTE_BACK, [
             (dict(logits=0), 1), (dict(ids=0), 1), (dict(dweights=0), 1), (dict(dlogits=0), 1), (dict(dlogits=A), 1),
-            (dict(top_k=65), 1), (dict(score=-1), 1), (dict(dtype=2), 2), (dict(dlogits=D + 8), 3)]),
+            (dict(top_k=65), 1), (dict(score=-1), 1), (dict(dtype=2), 2), (dict(dlogits=D + 8), 3),
+            (dict(tokens=1 << 25), 1)]),
         ("ns_experts_product", PRODUCT, [
             (dict(x=0), 1), (dict(w=0), 1), (dict(offsets=0), 1), (dict(y=0), 1), (dict(rows=0), 1),
             (dict(n_x=0), 1), (dict(fan_out=36), 3), (dict(fan_in=60), 3), (dict(ldx=68), 3), (dict(ldx=56), 1),
