@@ -702,3 +702,16 @@ def test_what_ran_is_named():
     finally:
         ns.ns_timing_enable(0)
         ns.ns_timing_reset()
+
+
+def test_example_learns_and_decodes():
+    import importlib.util
+    import pathlib
+    path = pathlib.Path(__file__).resolve().parent.parent / "examples" / "moe_sublayer.py"
+    spec = importlib.util.spec_from_file_location("moe_sublayer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    device()
+    losses, worst = example.main(["--tokens", "520", "--width", "136", "--hidden", "72", "--experts", "12", "--steps", "25"])
+    assert all(np.isfinite(losses)) and losses[-1] < 0.9 * losses[0]
+    assert worst == 0.0  # the same kernels on the same values
