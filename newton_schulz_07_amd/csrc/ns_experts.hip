@@ -471,8 +471,8 @@ ExpertsTile choose_tile(int dtype, ExpertsMode mode, const ExpertsArgs& g) {
   const int rows = g.n_rows / g.experts;  // an expert's, on average
   const bool few = mode != EXP_WEIGHT_GRAD && rows <= 16;
   if (dtype != 1) return few ? TILE_FEW : TILE_SMALL;
-  if (mode == EXP_PRODUCT && rows >= 256) return TILE_WIDE;
-  if (mode == EXP_WEIGHT_GRAD && most_tiles(mode, g, 256, 256) >= 768) return TILE_WIDE;
+  if (mode == EXP_PRODUCT && rows >= 256 && most_tiles(mode, g, 256, 256) >= 160) return TILE_WIDE;
+  if (mode == EXP_WEIGHT_GRAD && most_tiles(mode, g, 256, 256) >= 2304) return TILE_WIDE;
   if (mode == EXP_PRODUCT && few) return TILE_FEW;
   if (most_tiles(mode, g, 128, 256) >= 192) return TILE_LONG;
   return few ? TILE_FEW : TILE_SMALL;

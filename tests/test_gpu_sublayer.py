@@ -429,9 +429,10 @@ def some_rows(experts, most, seed):
 @pytest.mark.parametrize("counts,N,K,tiles", [
     # the larger tiles, ragged in rows and columns, with experts of no row, one and several stages
     (some_rows(100, 60, 1), 264, 520, ("128x256", "128x256", "128x256")),
-    (some_rows(200, 100, 2) + [0, 0, 1, 31, 32, 33, 64, 65], 520, 264, ("128x256", "128x256", "256x256")),
-    (some_rows(52, 700, 3), 1032, 776, ("256x256", "128x256", "256x256")),
-    ([300, 0, 513], 1288, 2056, ("256x256", "64x64", "128x256")),
+    (some_rows(200, 100, 2) + [0, 0, 1, 31, 32, 33, 64, 65], 520, 264, ("128x256", "128x256", "128x256")),
+    (some_rows(52, 700, 3), 1032, 776, ("256x256", "128x256", "128x256")),
+    ([300, 0, 513], 1288, 2056, ("64x64", "64x64", "128x256")),
+    (some_rows(580, 60, 4) + [0, 1, 33, 150], 264, 264, ("128x256", "128x256", "256x256")),
 ])
 def test_experts_large_tiles(counts, N, K, tiles, gather):
     dtype, dev = torch.bfloat16, device()
