@@ -14,6 +14,25 @@
 //                    gathered): k runs over the expert's rows
 // Sums are in fp32 and rounded once.
 //
+// bf16, 128 experts of 1536 x 2048, rows spread at random (us; TFLOP/s over the
+// rows that there are):
+//   65536 rows  product 503 (819), input gradient 485 (850), weight gradient 567 (727)
+//   16384 rows  product 230, input gradient 208, weight gradient 280
+//   32 rows     product 30 to 36: HBM or the last-level cache, the chosen
+//               experts are 179 MB
+// A large square library product reaches 1200 TFLOP/s here.  The product's
+// tiles of 256 rows are padded by 28 % at 512 rows to an expert and run at 1050;
+// the input gradient's of 128 rows by 12 %, and run at 950.  What bounds them is
+// the path from the L2 to the LDS (16 to 27 bytes a clock and CU): with more
+// stages in flight, the barrier moved or dead blocks skipped they take the same
+// time to 2 %.  The weight gradient has no padding, but its 16 stages do not
+// cover a tile's first loads and its stores: with the same rows in 16 experts
+// (128 stages) it takes 470, the others 390 and 424.  At 16384 rows the weights
+// and the output are 0.9 GB, and HBM bounds all three.
+// fp32 runs on the fp32 MFMA, a sixteenth of the rate: 999 rows of 7 experts of
+// 520 x 264 take 10, 14 and 12 us; one wave's 32 x 32 block over 520 columns of
+// k is 8 us of matrix instructions.
+//
 // The experts' row counts are known on the device only.  The grid holds the
 // most tiles that n_rows rows can make; every workgroup adds up the experts'
 // tiles (one prefix sum by each wave) and takes its own, or ends.
@@ -451,7 +470,22 @@ hipError_t launch_tiles(const ExpertsArgs& g, hipStream_t st) {
 }
 
 // Tiles of a launch: BM, BN, waves, 16-byte chunks of k, stages, workgroups
-// per CU.
+// per CU.  A large tile reads less for each product; a small one pads less and
+// makes more workgroups.  us, 1536 x 2048, bf16 if not said:
+//   256 x 256 against 128 x 256
+//     product          500 rows to each of 8 experts 50 / 38 (138 tiles at
+//                      most), 750 rows 51 / 64 (186), 1000 rows 57 / 68;
+//                      128 experts: 128 rows 268 / 246, 256 rows 355 / 361,
+//                      512 rows 518 / 558; 64 experts, 250 rows 191 / 178
+//     weight gradient  8, 16, 32, 64, 128 experts: 57 / 49, 85 / 79, 174 / 165,
+//                      200 / 212, 594 / 615 (48 tiles to an expert)
+//     input gradient   128 experts: 256 rows 315 / 296, 512 rows 502 / 487; 1000
+//                      rows of 8 experts 76 / 64: never 256 x 256
+//   128 x 256 against 64 x 64   400 rows of 8 experts 37 / 18, 2000 rows 42 / 52
+//   32 x 64   product: one row 14, against 35 with 128 x 256; 16 rows to each
+//             of 128 experts 147 / 157.  Input gradient: one row 12 / 29, 16 rows
+//             each 150 / 136.  fp32, 16 rows each: 394, with 64 x 64 434, with
+//             128 x 128 790; 2000 rows of 8 experts: 64 x 64 1085, 128 x 128 1321
 #define NS_EXPERTS_WIDE 256, 256, 2, 4, 8, 2, 1
 #define NS_EXPERTS_WIDE_GRAD 256, 256, 2, 4, 4, 3, 1
 #define NS_EXPERTS_LONG 128, 256, 2, 4, 4, 3, 2
@@ -504,9 +538,10 @@ hipError_t launch_mode(int dtype, const ExpertsArgs& g, hipStream_t st) {
 
 // ---------------------------------------------------------------- combine
 
-// out[t] = sum_j weights[t, j] y[slots[t, j]]: TPT threads to a token, each
-// walking its columns 8 at a time; eight rows are on their way before the
-// first is added.
+// out[t] = sum_j weights[t, j] y[slots[t, j]], in fp32, rounded once: TPT
+// threads to a token, each walking its columns 8 at a time; eight rows are on
+// their way before the first is added.  Bound by HBM: 8192 tokens x 8 rows of
+// 2048 bf16 take 83 us (3.6 TB/s; rows of 4 KB at random), 32 tokens 3.4 us.
 constexpr int kCombineAhead = 8;
 constexpr int kCombineBlocks = 1 << 20;  // a launch holds fewer than 2^32 threads: more tokens than that go round
 template <typename T, int TPT>
@@ -547,8 +582,10 @@ __global__ __launch_bounds__(256) void combine_kernel(const CombineArgs g) {
   }
 }
 
-// dy[slot] = weight dout[t],  dweights[t, j] = <dout[t], y[slot]>: a wave to a
-// token, eight choices at a time.
+// dy[slot] = weight dout[t],  dweights[t, j] = <dout[t], y[slot]> (fp32): a wave
+// to a token, eight choices at a time, so that dout is read once for them.
+// Bound by HBM: 107 us for the same (5.3 TB/s, y from the last-level cache in
+// part).
 template <typename T>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const CombineGradArgs g) {
   const int lane = threadIdx.x & 63, vpr = g.cols / 8;
@@ -640,6 +677,10 @@ static void launch_combine_of(int dtype, const CombineArgs& g, int pieces, hipSt
   if (dtype == 1) dispatch(combine_kernel<bf16, TPT>, grid, dim3(256), st, g);
   else dispatch(combine_kernel<float, TPT>, grid, dim3(256), st, g);
 }
+// As many threads to a token as its columns keep busy, at most a block: 4096
+// tokens of 128 columns 3.2 us with 16, 4.3 with 64, 4.5 with 256; of 512
+// columns 6.1 with 64, 6.4 with 256; 8192 of 2048 columns 45 with 256, 49 with
+// 64; 4 tokens of 2048 columns 2.9 and 6.2.
 hipError_t launch_combine(int dtype, const CombineArgs& g, hipStream_t st) {
   const int vpr = g.cols / 8;
   if (vpr > 64) launch_combine_of<256>(dtype, g, (vpr + 255) / 256, st);

@@ -35,8 +35,18 @@ struct LayerNormGradArgs {
 };
 
 // A row is held by tpr threads of vpt vectors of 8 elements (vpt 0: too long
-// for the registers).  A wave holds up to 2048 columns and needs no barrier
-// for its sums; longer rows take a whole block.
+// for the registers).  It goes by the row's length alone, so that a row's
+// result does not hang on how many rows there are.  A wave holds up to 2048
+// columns and needs no barrier for its sums; longer rows take a whole block,
+// of as few waves as hold the row.  Forward / backward us, as here and as the
+// next shape would have it (bf16):
+//   8192 x 1024   64 x 2    7.8 / 17    256 x 1   14 / 23
+//   8192 x 2048   64 x 4     14 / 26    256 x 1   16 / 27
+//   8192 x 4096   256 x 2    25 / 41    64 x 8    30 / 56
+//   8192 x 7168   256 x 4    38 / 79    1024 x 1  51 / 84
+//   2048 x 12288  1024 x 2   24 / 40    1024 x 4  37 / 270, 1024 x 0  29 / 245
+//   1024 x 32768  1024 x 4   33 / 196   1024 x 0  37 / 316
+// (1024 x 4 spills in the backward pass, and still beats reading rows again.)
 struct NormShape {
   int tpr, vpt;
 };
@@ -53,6 +63,9 @@ inline NormShape norm_shape(int cols) {
 }
 // columns of a row of partial sums: whole vectors
 NS_HD constexpr int partials_ld(int cols) { return (cols + 7) / 8 * 8; }
+// Blocks: enough to fill the card; in the backward pass as few as do, since
+// each leaves partial sums.  8192 x 7168 backward with 256 / 512 / 1024 blocks:
+// 85 / 79 / 89 us; 2048 x 16384, where one block fills a CU: 50 / 70 / 100 us.
 constexpr int kNormForwardBlocks = 2048, kNormBackwardBlocks = 512, kNormLongBackwardBlocks = 256;
 inline long long norm_blocks(long long rows, NormShape s, long long most) {
   const long long need = s.tpr == 64 ? (rows + 3) / 4 : rows;
@@ -76,6 +89,10 @@ hipError_t launch_layer_norm_backward(int dtype, const LayerNormGradArgs& g, int
 
 constexpr int kMaxExperts = 1024, kMaxTopK = 64, kMaxGroups = 64;
 constexpr int kRouteLeastWaves = 8, kRouteWaves = 16;  // waves of a routing block, where it is not the only one
+// Up to so many blocks each adds up the other blocks' counts itself, beyond
+// them a scan does: that costs a launch, the other time that grows with the
+// blocks.  16384 x 256 (256 blocks) 20.2 us without a scan, 22.3 with one;
+// 8192 x 512 (512 blocks) 42 and 33 us.
 constexpr int kRouteUnscannedBlocks = 256;
 // of the one block that few tokens take (with more than 256 experts 16 would spill registers)
 constexpr int route_single_waves(int experts) { return experts > 256 ? kRouteWaves / 2 : kRouteWaves; }
@@ -104,8 +121,13 @@ struct RouteGradArgs {
 };
 static_assert(route_single_waves(kMaxExperts) >= kRouteLeastWaves, "tokens for more than one block make more than one");
 // A token takes a whole wave, or 16 lanes where the tokens fill the card and
-// there are at most 256 experts.  A block has few waves as long as there are
-// at most kRouteUnscannedBlocks of them.
+// there are at most 256 experts: four tokens then share a wave's instructions,
+// while a lane has four times the experts to go through.  512 x 256: 13.4 us
+// with a wave each, 20.7 with 16 lanes; 4096 x 128: 13.2 and 15.3;
+// 16384 x 128: 35 and 18.  A block has few waves as long as there are at most
+// kRouteUnscannedBlocks blocks (8 waves and 16: 512 x 256 12.2 and 13.4 us,
+// 8192 x 256 20.3 and 23.2).  As many tokens as one block has waves take one
+// block and one launch (32 x 128 in two blocks 9.0 us, in one 12.5).
 struct RouteShape {
   int tokens_per_wave, waves, blocks, hist_ld;
 };
