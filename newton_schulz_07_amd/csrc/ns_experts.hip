@@ -104,8 +104,11 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ f32x4 acc_of(const f32x16& v, int rg) {  // 4 columns of a 32 x 32 block's row
   return f32x4{v[4 * rg], v[4 * rg + 1], v[4 * rg + 2], v[4 * rg + 3]};
 }
-// bf16 pairs of 4 columns
-__device__ __forceinline__ uint2 pack4(f32x4 v) { return make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])); }
+// bf16 pairs of 4 columns, each pair by one conversion
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint2 pack4(f32x4 v) {
+  return __builtin_bit_cast(uint2, __builtin_convertvector(v, bf16x4));
+}
 
 // The descriptor, in scalar registers (it is the same in every lane).
 __device__ __forceinline__ i32x4 uniform(i32x4 r) {
@@ -114,7 +117,8 @@ __device__ __forceinline__ i32x4 uniform(i32x4 r) {
   return u;
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, int MODE>
+// GATHER: the weight gradient's x is read through rows.
+template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, int MODE, bool GATHER>
 __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_kernel(const ExpertsArgs g) {
   constexpr bool PNAT = MODE == EXP_WEIGHT_GRAD, QNAT = MODE != EXP_PRODUCT;
   constexpr int NW = WM * WN, NT = NW * 64;
@@ -125,12 +129,13 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   constexpr int OCH = WTN / EPC, OPITCH = OCH + 1;  // chunks of a wave's output row, and of its place in the LDS
   constexpr int OUT = NW * 32 * OPITCH;             // 32 such rows for each wave
   constexpr bool WG = MODE == EXP_WEIGHT_GRAD;
+  static_assert(WG || !GATHER, "the other modes decide while they run");
   constexpr int RCP = BM / EPC, RCQ = BN / EPC;
   static_assert(WTM % 32 == 0 && WTN % 32 == 0, "wave tile must be whole 32x32 blocks");
   static_assert(LP % (64 * NW) == 0 && LQ % (64 * NW) == 0, "operands must split into whole wave loads");
   static_assert(ST >= 2 && NIW * (ST - 2) < 64, "ring depth");
   __shared__ uint4 lds[ST * STAGE > OUT ? ST * STAGE : OUT];  // the ring, then the output
-  __shared__ int row_ring[WG ? ST * NW * 64 : 1];  // see read_rows
+  __shared__ int row_ring[GATHER ? ST * NW * 64 : 1];  // see read_rows
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -222,7 +227,6 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   // range.
   constexpr int RPP = 64 / RCP, RPQ = 64 / RCQ, KRQ = NQ * RPQ;
   const unsigned ldp = (unsigned)(g.fan_out * ES), ldq = (unsigned)(g.ldx * ES);
-  const bool gather = WG && g.rows != nullptr;
   constexpr int SEENP = ES == 4 ? 8 : RCP % 16 == 0 ? 4 : 16, SEENQ = ES == 4 ? 8 : RCQ % 16 == 0 ? 4 : 16;
   constexpr int NCP = SEENP > RPP ? SEENP / RPP : 1, NCQ = SEENQ > RPQ ? SEENQ / RPQ : 1;
   static_assert(!WG || (NP % NCP == 0 && NQ % NCQ == 0), "a wave's first k row starts a period");
@@ -235,34 +239,45 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
       colp[t] = (unsigned)(min(i0 + src(t).row, M - EPC) * ES) + (unsigned)(lane / RCP) * ldp;
 #pragma unroll
     for (int t = 0; t < NCQ; ++t)
-      colq[t] = (unsigned)(min(j0 + src(NP + t).row, N - EPC) * ES) + (gather ? 0u : (unsigned)(lane / RCQ) * ldq);
+      colq[t] = (unsigned)(min(j0 + src(NP + t).row, N - EPC) * ES) + (GATHER ? 0u : (unsigned)(lane / RCQ) * ldq);
+    if constexpr (GATHER) rQ = uniform(make_rsrc(g.x, (unsigned)(g.n_x - 1) * ldq + (unsigned)(g.fan_in * ES)));
   }
   // x's row numbers: a wave keeps those of its own loads in the LDS, the KRQ of
   // stage kt at row_ring[kt % ST][wave].  They go out ST - 1 stages before the
   // loads that they are for, as one more load of that stage (LD in all), and
-  // have landed when those are issued: the wave has waited for its loads of
-  // stage kt - (ST - 1) by then.  (Scalar loads would return out of order with
-  // the fragment reads, each of which would wait for all of them.)
-  constexpr int LD = NIW + (WG ? 1 : 0);
+  // have landed a stage before those are issued: the wave has waited for its
+  // loads of stage kt - (ST - 1) by then.  take_rows reads them to registers
+  // ahead of that stage's last products.  (Scalar loads would return out of
+  // order with the fragment reads, each of which would wait for all of them.)
+  constexpr int LD = NIW + (GATHER ? 1 : 0);
   static_assert(!WG || KRQ <= 64, "one load holds a wave's row numbers");
-  const i32x4 rR = WG && gather ? uniform(make_rsrc(g.rows + tl.begin, (unsigned)K * 4u)) : i32x4{};
+  const i32x4 rR = GATHER ? uniform(make_rsrc(g.rows + tl.begin, (unsigned)K * 4u)) : i32x4{};
+  int row_of[GATHER ? NQ : 1];
   auto read_rows = [&](int kt, int slot) __attribute__((always_inline)) {
-    if constexpr (WG)
+    if constexpr (GATHER)
       dma4(lds_addr(reinterpret_cast<const uint4*>(row_ring + (slot * NW + wave) * 64)),
            (unsigned)(kt * BK + wave * KRQ + lane) * 4u, rR);  // past the expert's rows: zeros (not used)
   };
+  auto take_rows = [&](int slot) __attribute__((always_inline)) {
+    if constexpr (GATHER)
+#pragma unroll
+      for (int u = 0; u < NQ; ++u) row_of[u] = row_ring[(slot * NW + wave) * 64 + u * RPQ + lane / RCQ];
+  };
 
+  typedef std::integral_constant<int, 1> OfP;
+  typedef std::integral_constant<int, 2> OfQ;
   typedef std::integral_constant<int, 3> Both;
-  // what: 1 P's loads, 2 Q's, 3 both
-  auto issue = [&](int kt, int slot, auto what) __attribute__((always_inline)) {
-    constexpr bool DOP = decltype(what)::value & 1, DOQ = decltype(what)::value & 2;
+  // The loads of stage kt into a slot: P's, Q's or both.  whole: the stage has
+  // BK elements of k (known while compiling); otherwise that is looked at.
+  auto issue = [&](int kt, int slot, auto what, auto whole) __attribute__((always_inline)) {
+    constexpr bool DOP = decltype(what)::value & 1, DOQ = decltype(what)::value & 2, WHOLE = decltype(whole)::value;
     const int k0 = kt * BK;
     if constexpr (WG) {
-      const unsigned left = (unsigned)min(BK, K - k0);  // > 0
-      const T* dy = reinterpret_cast<const T*>(g.dy) + (size_t)(tl.begin + k0) * g.fan_out;
-      const T* x = reinterpret_cast<const T*>(g.x) + (gather ? 0 : (size_t)(tl.begin + k0) * g.ldx);
+      const unsigned left = WHOLE ? (unsigned)BK : (unsigned)min(BK, K - k0);  // > 0
+      const char* dy = reinterpret_cast<const char*>(g.dy) + (size_t)(unsigned)(tl.begin + k0) * ldp;
+      const char* x = reinterpret_cast<const char*>(g.x) + (size_t)(unsigned)(tl.begin + k0) * ldq;
       const i32x4 p = uniform(make_rsrc(dy, left * ldp));
-      const i32x4 q = uniform(make_rsrc(x, (gather ? (unsigned)g.n_x - 1 : left - 1) * ldq + (unsigned)(g.fan_in * ES)));
+      const i32x4 q = GATHER ? rQ : uniform(make_rsrc(x, (left - 1) * ldq + (unsigned)(g.fan_in * ES)));
 #pragma unroll
       for (int t = 0; t < NIW; ++t) {
         if (t < NP ? !DOP : !DOQ) continue;
@@ -270,25 +285,25 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
           dma16(lds_of(slot, t), colp[t % NCP] + (unsigned)(wave * NP + t) * RPP * ldp, p);
           continue;
         }
-        const int u = t - NP, kr = wave * KRQ + u * RPQ + lane / RCQ;
-        unsigned o;
-        if (gather) {
-          const int r = row_ring[(slot * NW + wave) * 64 + u * RPQ + lane / RCQ];
-          o = k0 + kr < K && (unsigned)r < (unsigned)g.n_x ? (unsigned)r * ldq : kOutOfRange;
-        } else {
-          o = (unsigned)(wave * NQ + u) * RPQ * ldq;
+        const int u = t - NP;
+        unsigned o = (unsigned)(wave * NQ + u) * RPQ * ldq;
+        if constexpr (GATHER) {
+          const int r = row_of[u], kr = wave * KRQ + u * RPQ + lane / RCQ;
+          const unsigned at = (unsigned)r * ldq;
+          const bool in = (WHOLE | (k0 + kr < K)) & ((unsigned)r < (unsigned)g.n_x);
+          o = in ? at : kOutOfRange;
         }
         dma16(lds_of(slot, t), o + colq[u % NCQ], q);
       }
-      if (DOQ && gather) read_rows(kt + ST - 1, (slot + ST - 1) % ST);
+      if (DOQ) read_rows(kt + ST - 1, (slot + ST - 1) % ST);
     } else {
-      const bool whole = k0 + BK <= K;
+      const bool all = WHOLE || k0 + BK <= K;
 #pragma unroll
       for (int t = 0; t < NIW; ++t) {
         if (t < NP ? !DOP : !DOQ) continue;
         // (an offset out of range stays there: kt steps are below 2^31)
         const unsigned o = off[t] + (unsigned)kt * (t < NP ? (unsigned)(BK * ES) : step_q);
-        dma16(lds_of(slot, t), whole || k0 + src(t).kpos < K ? o : kOutOfRange, t < NP ? rP : rQ);
+        dma16(lds_of(slot, t), all || k0 + src(t).kpos < K ? o : kOutOfRange, t < NP ? rP : rQ);
       }
     }
   };
@@ -345,28 +360,28 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   // publishes every wave's and certifies that this stage's slot is read out.
   const int nk = (K + BK - 1) / BK;
   uint4 pf[2][SM], qf[2][SN];
-  auto wait_stage = [&](int kt) __attribute__((always_inline)) {
+  auto wait_stage = [&](int kt, auto steady) __attribute__((always_inline)) {
     const int later = nk - 1 - kt;  // stages that may be in flight after kt, at most ST - 2
-    if (WG && !gather) {  // (NIW loads to a stage)
-      if (later >= ST - 2) wait_vm_lgkm0<NIW * (ST - 2)>();
-      else wait_vm_lgkm0<0>();
-    } else {
-      if (later >= ST - 2) wait_vm_lgkm0<LD * (ST - 2)>();
-      else if (ST > 4 && later == 2) wait_vm_lgkm0<LD * 2>();
-      else if (ST > 3 && later == 1) wait_vm_lgkm0<LD * 1>();
-      else wait_vm_lgkm0<0>();
-    }
+    if (decltype(steady)::value || later >= ST - 2) wait_vm_lgkm0<LD * (ST - 2)>();
+    else if (ST > 4 && later == 2) wait_vm_lgkm0<LD * 2>();
+    else if (ST > 3 && later == 1) wait_vm_lgkm0<LD * 1>();
+    else wait_vm_lgkm0<0>();
     ring_barrier();
   };
   static_assert(ST <= 5 && KS % 2 == 0, "tail waits; fragment buffers alternate");
-  auto stage = [&](int kt, int u) __attribute__((always_inline)) {
-    if (kt + ST - 1 < nk) issue(kt + ST - 1, (u + ST - 1) % ST, Both());
+  // steady: more than ST stages follow, so that nothing has to be looked at
+  // (branches and waits between the products of a stage are time that the
+  // other waves, stopped by the same barrier, cannot fill).
+  auto stage = [&](int kt, int u, auto steady) __attribute__((always_inline)) {
+    constexpr bool STEADY = decltype(steady)::value;
+    if (STEADY || kt + ST - 1 < nk) issue(kt + ST - 1, (u + ST - 1) % ST, Both(), steady);
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       if (s + 1 < KS) {
         load_step(u, s + 1, pf[(s + 1) & 1], qf[(s + 1) & 1]);
-      } else if (kt + 1 < nk) {
-        wait_stage(kt + 1);
+      } else if (STEADY || kt + 1 < nk) {
+        wait_stage(kt + 1, steady);
+        take_rows(u % ST);  // stage kt + ST's
         load_step((u + 1) % ST, 0, pf[0], qf[0]);
       }
       __builtin_amdgcn_sched_barrier(0);  // keeps these reads ahead of the MFMAs
@@ -376,40 +391,44 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
         for (int b = 0; b < SN; ++b) mfma_chunk(acc[a][b], qf[s & 1][b], pf[s & 1][a], T());
     }
   };
-  if (WG && gather) {
+  if constexpr (GATHER) {
     if (nk > 0) {  // P's first loads do not wait for the row numbers
 #pragma unroll
       for (int s = 0; s < ST - 1; ++s) read_rows(s, s);
 #pragma unroll
       for (int s = 0; s < ST - 1; ++s)
-        if (s < nk) issue(s, s, std::integral_constant<int, 1>());
+        if (s < nk) issue(s, s, OfP(), std::false_type());
       if (nk >= ST - 1) wait_vm_lgkm0<NP * (ST - 1)>();
       else wait_vm_lgkm0<0>();
       asm volatile("" ::: "memory");
     }
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s)
-      if (s < nk) issue(s, s, std::integral_constant<int, 2>());
-    static_assert(!WG || ST <= 3, "the first wait");
+      if (s < nk) {
+        take_rows(s);
+        issue(s, s, OfQ(), std::false_type());
+      }
+    static_assert(ST <= 3, "the first wait");
     if (nk > 1) wait_vm_lgkm0<(NQ + 1) * (ST - 2)>();  // Q's loads of stage 1
     else wait_vm_lgkm0<0>();
   } else {
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s)
-      if (s < nk) issue(s, s, Both());
+      if (s < nk) issue(s, s, Both(), std::false_type());
   }
   if (nk > 0) {
-    wait_stage(0);
+    wait_stage(0, std::false_type());
+    take_rows(ST - 1);
     load_step(0, 0, pf[0], qf[0]);
   }
   int kt0 = 0;
-  for (; kt0 + ST <= nk; kt0 += ST) {
+  for (; kt0 + 2 * ST - 1 < nk; kt0 += ST) {
 #pragma unroll
-    for (int u = 0; u < ST; ++u) stage(kt0 + u, u);
+    for (int u = 0; u < ST; ++u) stage(kt0 + u, u, std::true_type());
   }
 #pragma unroll
-  for (int u = 0; u < ST - 1; ++u)
-    if (kt0 + u < nk) stage(kt0 + u, u);
+  for (int u = 0; u < 2 * ST - 1; ++u)
+    if (kt0 + u < nk) stage(kt0 + u, u % ST, std::false_type());
   wait_vm_lgkm0<0>();  // (row numbers that nothing asked for may still be on their way)
   __syncthreads();
 
@@ -465,7 +484,10 @@ hipError_t launch_tiles(const ExpertsArgs& g, hipStream_t st) {
   }
   if (grid <= 0) return hipSuccess;
   if (grid > 0x7fffffffll) return hipErrorInvalidValue;
-  dispatch(experts_kernel<T, BM, BN, WM, WN, CPR, ST, OCC, MODE>, dim3((unsigned)grid, (unsigned)experts), dim3(WM * WN * 64), st, g);
+  const dim3 blocks((unsigned)grid, (unsigned)experts), threads(WM * WN * 64);
+  constexpr bool WG = MODE == EXP_WEIGHT_GRAD;
+  if (WG && g.rows != nullptr) dispatch(experts_kernel<T, BM, BN, WM, WN, CPR, ST, OCC, MODE, WG>, blocks, threads, st, g);
+  else dispatch(experts_kernel<T, BM, BN, WM, WN, CPR, ST, OCC, MODE, false>, blocks, threads, st, g);
   return hipGetLastError();
 }
 
