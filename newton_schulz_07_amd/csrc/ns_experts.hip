@@ -16,19 +16,19 @@
 //
 // bf16, 128 experts of 1536 x 2048, rows spread at random (us; TFLOP/s over the
 // rows that there are):
-//   65536 rows  product 503 (819), input gradient 485 (850), weight gradient 567 (727)
-//   16384 rows  product 230, input gradient 208, weight gradient 280
-//   32 rows     product 30 to 36: HBM or the last-level cache, the chosen
+//   65536 rows  product 495 (833), input gradient 480 (859), weight gradient 535 (771)
+//   16384 rows  product 238, input gradient 206, weight gradient 262
+//   32 rows     product 28 to 36: HBM or the last-level cache, the chosen
 //               experts are 179 MB
-// A large square library product reaches 1200 TFLOP/s here.  The product's
-// tiles of 256 rows are padded by 28 % at 512 rows to an expert and run at 1050;
-// the input gradient's of 128 rows by 12 %, and run at 950.  What bounds them is
-// the path from the L2 to the LDS (16 to 27 bytes a clock and CU): with more
-// stages in flight, the barrier moved or dead blocks skipped they take the same
-// time to 2 %.  The weight gradient has no padding, but its 16 stages do not
-// cover a tile's first loads and its stores: with the same rows in 16 experts
-// (128 stages) it takes 470, the others 390 and 424.  At 16384 rows the weights
-// and the output are 0.9 GB, and HBM bounds all three.
+//   65536 rows, 16 experts  375 (1100), 422 (977), 370 (1114)
+// A large square library product reaches 1200 TFLOP/s here.  At 512 rows to an
+// expert the product's tiles of 256 rows are padded by 28 %, the input
+// gradient's of 128 rows by 12 %, and the weight gradient's 16 stages do not
+// cover a tile's first loads and its stores.  The stages themselves are bound
+// by the path from the L2 to the LDS (16 to 27 bytes a clock and CU; the matrix
+// cores are busy 53 to 58 % of the time): with more stages in flight or dead
+// blocks skipped they take the same time to 2 %.  At 16384 rows the weights and
+// the output are 0.9 GB, and HBM bounds all three.
 // fp32 runs on the fp32 MFMA, a sixteenth of the rate: 999 rows of 7 experts of
 // 520 x 264 take 10, 14 and 12 us; one wave's 32 x 32 block over 520 columns of
 // k is 8 us of matrix instructions.
@@ -495,12 +495,13 @@ hipError_t launch_tiles(const ExpertsArgs& g, hipStream_t st) {
 // per CU.  A large tile reads less for each product; a small one pads less and
 // makes more workgroups.  us, 1536 x 2048, bf16 if not said:
 //   256 x 256 against 128 x 256
-//     product          500 rows to each of 8 experts 50 / 38 (138 tiles at
-//                      most), 750 rows 51 / 64 (186), 1000 rows 57 / 68;
-//                      128 experts: 128 rows 268 / 246, 256 rows 355 / 361,
-//                      512 rows 518 / 558; 64 experts, 250 rows 191 / 178
-//     weight gradient  8, 16, 32, 64, 128 experts: 57 / 49, 85 / 79, 174 / 165,
-//                      200 / 212, 594 / 615 (48 tiles to an expert)
+//     product          500 rows to each of 8 experts 49 / 37 (138 tiles at
+//                      most), 750 rows 51 / 64 (186), 1000 rows 55 / 67;
+//                      128 experts: 128 rows 263 / 238, 256 rows 344 / 347,
+//                      512 rows 495 / 541; 64 experts, 250 rows 178 / 164
+//     weight gradient  4096 rows to each of 16 experts 370 / 415, 512 of 128
+//                      533 / 538, 500 of 32 137 / 132, 128 of 128 268 / 262;
+//                      1000 rows of 8 78 / 65 (384 tiles)
 //     input gradient   128 experts: 256 rows 315 / 296, 512 rows 502 / 487; 1000
 //                      rows of 8 experts 76 / 64: never 256 x 256
 //   128 x 256 against 64 x 64   400 rows of 8 experts 37 / 18, 2000 rows 42 / 52
@@ -528,7 +529,7 @@ ExpertsTile choose_tile(int dtype, ExpertsMode mode, const ExpertsArgs& g) {
   const bool few = mode != EXP_WEIGHT_GRAD && rows <= 16;
   if (dtype != 1) return few ? TILE_FEW : TILE_SMALL;
   if (mode == EXP_PRODUCT && rows >= 256 && most_tiles(mode, g, 256, 256) >= 160) return TILE_WIDE;
-  if (mode == EXP_WEIGHT_GRAD && most_tiles(mode, g, 256, 256) >= 2304) return TILE_WIDE;
+  if (mode == EXP_WEIGHT_GRAD && rows >= 1024 && most_tiles(mode, g, 256, 256) >= 768) return TILE_WIDE;
   if (mode == EXP_PRODUCT && few) return TILE_FEW;
   if (most_tiles(mode, g, 128, 256) >= 192) return TILE_LONG;
   return few ? TILE_FEW : TILE_SMALL;

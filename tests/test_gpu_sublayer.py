@@ -432,7 +432,7 @@ def some_rows(experts, most, seed):
     (some_rows(200, 100, 2) + [0, 0, 1, 31, 32, 33, 64, 65], 520, 264, ("128x256", "128x256", "128x256")),
     (some_rows(52, 700, 3), 1032, 776, ("256x256", "128x256", "128x256")),
     ([300, 0, 513], 1288, 2056, ("64x64", "64x64", "128x256")),
-    (some_rows(580, 60, 4) + [0, 1, 33, 150], 264, 264, ("128x256", "128x256", "256x256")),
+    (some_rows(580, 60, 4) + [0, 1, 33, 150], 264, 264, ("128x256", "128x256", "128x256")),
 ])
 def test_experts_large_tiles(counts, N, K, tiles, gather):
     dtype, dev = torch.bfloat16, device()
@@ -456,6 +456,25 @@ def test_experts_large_tiles(counts, N, K, tiles, gather):
         dw = ns.ns_experts_weight_grad(dyg, xg, og, rg)
         assert "tile=" + tiles[2] in ns.ns_query_last_config()
         products_near(dw, want, mag, max(counts), dtype)
+
+
+@pytest.mark.parametrize("gather", [True, False])
+def test_experts_weight_grad_of_many_rows(gather):
+    # 256x256 tiles, ragged, with experts of no row, one stage and several turns of the ring
+    counts = [3000, 0, 1, 2500, 33, 1024, 1400, 97, 2222, 64, 31, 2101]
+    N, K, dtype, dev = 2056, 1800, torch.bfloat16, device()
+    M = sum(counts)
+    n_x = M // 2 if gather else M
+    offsets, rows = routed(counts, n_x, 184)
+    x, dy = normal((n_x, K), 185, dtype).to(dev), normal((M, N), 186, dtype).to(dev)
+    for _ in range(3):
+        dw = ns.ns_experts_weight_grad(dy, x, offsets.to(dev), rows.to(dev) if gather else None)
+        assert "tile=256x256" in ns.ns_query_last_config()
+        for e, c in enumerate(counts):  # (in 64 bits, on the GPU)
+            b = int(offsets[e])
+            X = x[rows[b:b + c].to(dev).long() if gather else slice(b, b + c)].double()
+            D = dy[b:b + c].double()
+            products_near(dw[e], to64(D.t() @ X), to64(D.abs().t() @ X.abs()), c, dtype)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
