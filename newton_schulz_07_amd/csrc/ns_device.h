@@ -126,12 +126,42 @@ __device__ __forceinline__ void dma16(unsigned lds_byte_addr, unsigned voff, i32
                : "memory", "m0");
 }
 
+// The same for data that no other workgroup reads: its lines make room in the
+// L2 first.
+__device__ __forceinline__ void dma16_once(unsigned lds_byte_addr, unsigned voff, i32x4 rsrc) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+               :
+               : "s"(lds_byte_addr), "v"(voff), "s"(rsrc)
+               : "memory", "m0");
+}
+
 // The same, 4 bytes per lane at m0 + 4 * lane.
 __device__ __forceinline__ void dma4(unsigned lds_byte_addr, unsigned voff, i32x4 rsrc) {
   asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :
                : "s"(lds_byte_addr), "v"(voff), "s"(rsrc)
                : "memory", "m0");
+}
+
+// *p = v, in pieces of 16 bytes.  stream: as part of an output that the L2
+// could not keep anyway; its lines then leave at once, in place of what other
+// workgroups still read there.
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+template <typename V> __device__ __forceinline__ void store_whole(V* p, const V& v, bool stream) {
+  constexpr int N = sizeof(V) / 16;
+  static_assert(sizeof(V) % 16 == 0, "whole 16-byte pieces");
+  u32x4 w[N];
+  __builtin_memcpy(w, &v, sizeof(V));
+  u32x4* to = reinterpret_cast<u32x4*>(p);
+  if (stream) {
+    asm volatile("");  // (the compiler would make one plain store of both kinds)
+#pragma unroll
+    for (int i = 0; i < N; ++i) __builtin_nontemporal_store(w[i], to + i);
+    asm volatile("");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) to[i] = w[i];
+  }
 }
 
 __device__ __forceinline__ unsigned lds_addr(const uint4* p) {

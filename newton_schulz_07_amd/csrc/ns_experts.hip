@@ -117,8 +117,9 @@ __device__ __forceinline__ i32x4 uniform(i32x4 r) {
   return u;
 }
 
-// GATHER: the weight gradient's x is read through rows.
-template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, int MODE, bool GATHER>
+// GATHER: the weight gradient's x is read through rows.  ONCE: the weights are
+// more than the L2s hold, and few rows read each.
+template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, int MODE, bool GATHER, bool ONCE>
 __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_kernel(const ExpertsArgs g) {
   constexpr bool PNAT = MODE == EXP_WEIGHT_GRAD, QNAT = MODE != EXP_PRODUCT;
   constexpr int NW = WM * WN, NT = NW * 64;
@@ -303,7 +304,10 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
         if (t < NP ? !DOP : !DOQ) continue;
         // (an offset out of range stays there: kt steps are below 2^31)
         const unsigned o = off[t] + (unsigned)kt * (t < NP ? (unsigned)(BK * ES) : step_q);
-        dma16(lds_of(slot, t), all || k0 + src(t).kpos < K ? o : kOutOfRange, t < NP ? rP : rQ);
+        const unsigned at = all || k0 + src(t).kpos < K ? o : kOutOfRange;
+        if (t < NP) dma16(lds_of(slot, t), at, rP);
+        else if constexpr (ONCE) dma16_once(lds_of(slot, t), at, rQ);
+        else dma16(lds_of(slot, t), at, rQ);
       }
     }
   };
@@ -462,14 +466,14 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
       const int r = (c0 + lane) / OCH, c = (c0 + lane) % OCH;
       const int i = i0 + wm * WTM + a * 32 + r, j = j0 + wn * WTN + c * EPC;
       const uint4 v = mine[r * OPITCH + c];
-      if (i < m_end && j < N) *reinterpret_cast<uint4*>(O + (size_t)i * N + j) = v;
+      if (i < m_end && j < N) store_whole(reinterpret_cast<uint4*>(O + (size_t)i * N + j), v, g.stream);
     }
     __builtin_amdgcn_wave_barrier();
   }
 }
 
 template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, int MODE>
-hipError_t launch_tiles(const ExpertsArgs& g, hipStream_t st) {
+hipError_t launch_tiles(ExpertsArgs g, hipStream_t st) {
   const int N = MODE == EXP_PRODUCT ? g.fan_out : g.fan_in;
   const long long tiles_n = (N + BN - 1) / BN;
   long long grid, experts = 1;
@@ -485,9 +489,15 @@ hipError_t launch_tiles(const ExpertsArgs& g, hipStream_t st) {
   if (grid <= 0) return hipSuccess;
   if (grid > 0x7fffffffll) return hipErrorInvalidValue;
   const dim3 blocks((unsigned)grid, (unsigned)experts), threads(WM * WN * 64);
-  constexpr bool WG = MODE == EXP_WEIGHT_GRAD;
-  if (WG && g.rows != nullptr) dispatch(experts_kernel<T, BM, BN, WM, WN, CPR, ST, OCC, MODE, WG>, blocks, threads, st, g);
-  else dispatch(experts_kernel<T, BM, BN, WM, WN, CPR, ST, OCC, MODE, false>, blocks, threads, st, g);
+  constexpr bool WG = MODE == EXP_WEIGHT_GRAD, FEW = !WG && BM == 32;
+  const long long weights = (long long)g.experts * g.fan_out * g.fan_in * (long long)sizeof(T);
+  g.stream = beyond_l2(WG ? weights : (long long)g.n_rows * N * (long long)sizeof(T));
+#define NS_EXPERTS(GATHER, ONCE) \
+  dispatch(experts_kernel<T, BM, BN, WM, WN, CPR, ST, OCC, MODE, GATHER, ONCE>, blocks, threads, st, g)
+  if (WG && g.rows != nullptr) NS_EXPERTS(WG, false);
+  else if (FEW && beyond_l2(weights)) NS_EXPERTS(false, FEW);
+  else NS_EXPERTS(false, false);
+#undef NS_EXPERTS
   return hipGetLastError();
 }
 
@@ -600,7 +610,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const CombineArgs g) {
           for (int e = 0; e < 8; ++e) s[e] = fmaf(w[u], f[e], s[e]);
         }
       }
-      reinterpret_cast<Raw8<T>*>(g.out)[(size_t)t * vpr + v] = pack8(s, T());
+      store_whole(reinterpret_cast<Raw8<T>*>(g.out) + (size_t)t * vpr + v, pack8(s, T()), g.stream);
     }
   }
 }
@@ -645,7 +655,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const CombineGrad
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = w[u] * d[e];
-            dy[(size_t)slot[u] * vpr + v] = pack8(f, T());
+            store_whole(dy + (size_t)slot[u] * vpr + v, pack8(f, T()), g.stream);
           }
         }
         if (g.dweights) {
@@ -704,7 +714,9 @@ static void launch_combine_of(int dtype, const CombineArgs& g, int pieces, hipSt
 // tokens of 128 columns 3.2 us with 16, 4.3 with 64, 4.5 with 256; of 512
 // columns 6.1 with 64, 6.4 with 256; 8192 of 2048 columns 45 with 256, 49 with
 // 64; 4 tokens of 2048 columns 2.9 and 6.2.
-hipError_t launch_combine(int dtype, const CombineArgs& g, hipStream_t st) {
+hipError_t launch_combine(int dtype, const CombineArgs& args, hipStream_t st) {
+  CombineArgs g = args;
+  g.stream = beyond_l2((long long)g.tokens * g.cols * (dtype == 1 ? 2 : 4));
   const int vpr = g.cols / 8;
   if (vpr > 64) launch_combine_of<256>(dtype, g, (vpr + 255) / 256, st);
   else if (vpr > 16) launch_combine_of<64>(dtype, g, 1, st);
@@ -712,7 +724,9 @@ hipError_t launch_combine(int dtype, const CombineArgs& g, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_combine_backward(int dtype, const CombineGradArgs& g, hipStream_t st) {
+hipError_t launch_combine_backward(int dtype, const CombineGradArgs& args, hipStream_t st) {
+  CombineGradArgs g = args;
+  g.stream = beyond_l2((long long)g.n_rows * g.cols * (dtype == 1 ? 2 : 4));
   const dim3 grid((unsigned)std::min(kCombineBlocks, (g.tokens + 3) / 4));
   if (dtype == 1) dispatch(combine_backward_kernel<bf16>, grid, dim3(256), st, g);
   else dispatch(combine_backward_kernel<float>, grid, dim3(256), st, g);

@@ -49,10 +49,10 @@ __device__ __forceinline__ Raw8<T> load8(const T* row, int t, int i, int cols) {
   return r;
 }
 template <typename T, int TPR, int HOW>
-__device__ __forceinline__ void store8(T* row, int t, int i, int cols, const float* f) {
+__device__ __forceinline__ void store8(T* row, int t, int i, int cols, const float* f, bool stream) {
   const Raw8<T> r = pack8(f, T());
   if (HOW != kSingles) {  // (outputs are contiguous: whole vectors are aligned)
-    if (column<TPR, HOW>(t, i, 0) < cols) reinterpret_cast<Raw8<T>*>(row)[t + i * TPR] = r;
+    if (column<TPR, HOW>(t, i, 0) < cols) store_whole(reinterpret_cast<Raw8<T>*>(row) + t + i * TPR, r, stream);
   } else {
     T x[8];
     __builtin_memcpy(x, &r, sizeof(r));
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void layer_norm_kernel(const
       unpack8(r[i], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[i][e], b[i][e]);
-      store8<T, TPR, HOW>(y, t, i, g.cols, f);
+      store8<T, TPR, HOW>(y, t, i, g.cols, f, g.stream);
     }
     if (t == 0) {
       if (g.mean) g.mean[row] = mean;
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(const LayerNormAr
       unpack8(load8<T, 1024, HOW>(x, t, i, g.cols), f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[0][e], b[0][e]);
-      store8<T, 1024, HOW>(y, t, i, g.cols, f);
+      store8<T, 1024, HOW>(y, t, i, g.cols, f, g.stream);
     }
     if (t == 0) {
       if (g.mean) g.mean[row] = mean;
@@ -261,7 +261,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void layer_norm_backward_ker
           const float xh = (fx[e] - mean) * rstd;
           fx[e] = rstd * (fmaf(fd[e], w[i][e], -c1) - xh * c2);
         }
-        store8<T, TPR, HOW>(dx, t, i, g.cols, fx);
+        store8<T, TPR, HOW>(dx, t, i, g.cols, fx, g.stream);
       }
     }
   }
@@ -290,7 +290,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void layer_norm_backward_ker
 #pragma unroll
           for (int r = 0; r < RPB - 1; ++r) x[e] += part[r][(i * 8 + e) * TPR + t];
       }
-      store8<float, TPR, HOW>(out + (size_t)h * ld, t, i, g.cols, x);
+      store8<float, TPR, HOW>(out + (size_t)h * ld, t, i, g.cols, x, false);
     }
   }
 }
@@ -343,7 +343,7 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_long_kernel(const La
         const float xh = (fx[e] - mean) * rstd;
         fx[e] = rstd * (fmaf(fd[e], w[0][e], -c1) - xh * c2);
       }
-      store8<T, 1024, HOW>(dx, t, i, g.cols, fx);
+      store8<T, 1024, HOW>(dx, t, i, g.cols, fx, g.stream);
     }
   }
 }
@@ -413,7 +413,9 @@ void launch_backward(const LayerNormGradArgs& g, int blocks, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_layer_norm(int dtype, const LayerNormArgs& g, hipStream_t st) {
+hipError_t launch_layer_norm(int dtype, const LayerNormArgs& args, hipStream_t st) {
+  LayerNormArgs g = args;
+  g.stream = beyond_l2(g.rows * g.cols * (dtype == 1 ? 2 : 4));
   const int how = g.cols % 8 != 0 ? kSingles : g.ldx % 8 != 0 ? kVectors : kAligned;
   if (dtype == 1)
     how == kAligned ? launch_forward<bf16, kAligned>(g, st)
@@ -424,7 +426,9 @@ hipError_t launch_layer_norm(int dtype, const LayerNormArgs& g, hipStream_t st) 
   return hipGetLastError();
 }
 
-hipError_t launch_layer_norm_backward(int dtype, const LayerNormGradArgs& g, int blocks, hipStream_t st) {
+hipError_t launch_layer_norm_backward(int dtype, const LayerNormGradArgs& args, int blocks, hipStream_t st) {
+  LayerNormGradArgs g = args;
+  g.stream = beyond_l2(g.rows * g.cols * (dtype == 1 ? 2 : 4));
   if (blocks > 0) {
     const int how = g.cols % 8 != 0 ? kSingles : g.ldx % 8 != 0 || g.lddy % 8 != 0 ? kVectors : kAligned;
     if (dtype == 1)

@@ -12,6 +12,13 @@
 
 namespace ns {
 
+// Whether an array is more than the L2s hold (8 of 4 MiB).  Outputs that are
+// then leave them at once (store_whole): layer norm and gradient of 8192 x 7168
+// bf16 111 us, 123 without; combine's gradient of 8192 x 8 rows of 2048 and its
+// forward pass 175 and 189; the weight gradient of 128 x 1536 x 2048 from 65536
+// rows 452 and 532, from 16384 rows 201 and 262, from 32 rows 138 and 136.
+inline bool beyond_l2(long long bytes) { return bytes > (32ll << 20); }
+
 // ------------------------------------------------------------ layer norm
 
 struct LayerNormArgs {
@@ -22,6 +29,7 @@ struct LayerNormArgs {
   long long rows, ldx;
   int cols, param_dtype;
   float eps;
+  bool stream;  // y is beyond_l2 (set at the launch, as below)
 };
 struct LayerNormGradArgs {
   const void *dy, *x;  // rows lddy / ldx elements apart
@@ -32,6 +40,7 @@ struct LayerNormGradArgs {
   float* partials;     // [blocks][2][cols], null if neither dw nor db is wanted
   long long rows, lddy, ldx;
   int cols, param_dtype;
+  bool stream;
 };
 
 // A row is held by tpr threads of vpt vectors of 8 elements (vpt 0: too long
@@ -170,6 +179,7 @@ struct ExpertsArgs {
   const int* rows;     // [n_rows], or null: row i of x
   long long ldx;
   int n_x, n_rows, experts, fan_out, fan_in;
+  bool stream;
 };
 // What launch_experts runs, for ns_query_last_config: a format of the type's
 // name, n_rows, experts, fan_out and fan_in.
@@ -184,6 +194,7 @@ struct CombineArgs {
   const float* weights;  // [tokens, top_k], or null: 1
   void* out;             // [tokens, cols]
   int tokens, top_k, n_rows, cols;
+  bool stream;
 };
 struct CombineGradArgs {
   const void *dout, *y;
@@ -192,6 +203,7 @@ struct CombineGradArgs {
   void* dy;         // [n_rows, cols], or null
   float* dweights;  // [tokens, top_k], or null
   int tokens, top_k, n_rows, cols;
+  bool stream;
 };
 hipError_t launch_combine(int dtype, const CombineArgs& g, hipStream_t st);
 hipError_t launch_combine_backward(int dtype, const CombineGradArgs& g, hipStream_t st);

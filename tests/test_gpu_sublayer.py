@@ -616,6 +616,75 @@ def test_combine_bad_slots_add_nothing():
     assert dw[0, 1] == 0 and dw[2, 0] == 0 and (dw[3] == 0).all() and (dy[9:] == 0).all()
 
 
+# --------------------------------------------- outputs beyond the L2 (32 MiB)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_layer_norm_of_many_rows_is_that_of_few(dtype):
+    dev = device()
+    x, dy = normal((5003, 4104), 140, dtype).to(dev), normal((5003, 4104), 141, dtype).to(dev)
+    w, b = normal((4104,), 142).to(dev), normal((4104,), 143).to(dev)
+    y, mean, rstd = ns.ns_layer_norm(x, w, b)
+    dx, dw, db = ns.ns_layer_norm_backward(dy, x, w, mean, rstd)
+    assert y.numel() * y.element_size() > 32 << 20
+    for i in range(0, 5003, 1000):
+        s = slice(i, i + 1000)
+        ys, ms, rs = ns.ns_layer_norm(x[s], w, b)
+        assert torch.equal(ys, y[s]) and torch.equal(ms, mean[s]) and torch.equal(rs, rstd[s])
+        assert torch.equal(ns.ns_layer_norm_backward(dy[s], x[s], w, ms, rs)[0], dx[s])
+    xh = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    terms = dy.double() * xh
+    # xh is off by 3 U of itself and of mean rstd; a sum of 5003 terms
+    near(dw, to64(terms.sum(0)), 5100 * U * to64((terms.abs() + dy.double().abs()).sum(0)))
+    near(db, to64(dy.double().sum(0)), 5100 * U * to64(dy.double().abs().sum(0)))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_experts_products_of_many_rows(dtype):
+    dev = device()
+    counts, N, K = [4000, 0, 33, 5100, 1], 2056, 1992
+    offsets, rows = routed(counts, 3000, 144)
+    x, w = normal((3000, K), 145, dtype).to(dev), normal((5, N, K), 146, dtype).to(dev)
+    dy = normal((sum(counts), N), 147, dtype).to(dev)
+    y = ns.ns_experts_product(x, w, offsets.to(dev), rows.to(dev))
+    dx = ns.ns_experts_input_grad(dy, w, offsets.to(dev))
+    assert dx.numel() * dx.element_size() > 32 << 20
+    for e, c in enumerate(counts):  # (in 64 bits, on the GPU)
+        s = slice(int(offsets[e]), int(offsets[e]) + c)
+        X, W, D = x[rows[s].to(dev).long()].double(), w[e].double(), dy[s].double()
+        products_near(y[s], to64(X @ W.t()), to64(X.abs() @ W.abs().t()), K, dtype)
+        products_near(dx[s], to64(D @ W), to64(D.abs() @ W.abs()), N, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_experts_few_rows_of_many_weights(dtype):
+    dev = device()
+    counts, N, K = ([3, 0, 40, 1, 2, 0, 9, 1] * 9), 520, 520
+    M, E = sum(counts), len(counts)
+    offsets, rows = routed(counts, 50, 148)
+    x, w, dy = normal((50, K), 149, dtype), normal((E, N, K), 150, dtype), normal((M, N), 151, dtype)
+    assert w.numel() * w.element_size() > 32 << 20
+    X, W, D, R, O = to64(x), to64(w), to64(dy), rows.numpy(), offsets.numpy()
+    y = ns.ns_experts_product(x.to(dev), w.to(dev), offsets.to(dev), rows.to(dev))
+    assert "tile=32x64" in ns.ns_query_last_config()
+    products_near(y, ref.experts_product(X, W, O, R), ref.experts_product(abs(X), abs(W), O, R), K, dtype)
+    dx = ns.ns_experts_input_grad(dy.to(dev), w.to(dev), offsets.to(dev))
+    products_near(dx, ref.experts_input_grad(D, W, O), ref.experts_input_grad(abs(D), abs(W), O), N, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_combine_backward_of_many_rows(dtype):
+    dev = device()
+    T, k, cols = 3001, 3, 2056
+    slots = torch.randperm(T * k, generator=torch.Generator().manual_seed(152)).int().view(T, k).to(dev)
+    y, dout, w = normal((T * k, cols), 153, dtype).to(dev), normal((T, cols), 154, dtype).to(dev), normal((T, k), 155).to(dev)
+    dy, dw = ns.ns_experts_combine_backward(dout, y, slots, w)
+    assert dy.numel() * dy.element_size() > 32 << 20
+    assert torch.equal(dy[slots.long()], (w[:, :, None] * dout.float()[:, None]).to(dtype))  # one product, rounded
+    terms = dout.double()[:, None] * y[slots.long()].double()
+    near(dw, to64(terms.sum(2)), cols * U * to64(terms.abs().sum(2)))
+
+
 # ------------------------------------------------------- streams, graphs
 
 
