@@ -3,6 +3,8 @@
 // transposed fragment reads.
 #pragma once
 
+#include <type_traits>
+
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -143,24 +145,31 @@ __device__ __forceinline__ void dma4(unsigned lds_byte_addr, unsigned voff, i32x
                : "memory", "m0");
 }
 
-// *p = v, in pieces of 16 bytes.  stream: as part of an output that the L2
-// could not keep anyway; its lines then leave at once, in place of what other
+// *p = v, in pieces of 16 bytes.  STREAM: as part of an output that the L2 could
+// not keep anyway; its lines then leave at once, in place of what other
 // workgroups still read there.
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-template <typename V> __device__ __forceinline__ void store_whole(V* p, const V& v, bool stream) {
+template <bool STREAM, typename V> __device__ __forceinline__ void store_whole(V* p, const V& v) {
   constexpr int N = sizeof(V) / 16;
   static_assert(sizeof(V) % 16 == 0, "whole 16-byte pieces");
   u32x4 w[N];
   __builtin_memcpy(w, &v, sizeof(V));
   u32x4* to = reinterpret_cast<u32x4*>(p);
-  if (stream) {
-    asm volatile("");  // (the compiler would make one plain store of both kinds)
 #pragma unroll
-    for (int i = 0; i < N; ++i) __builtin_nontemporal_store(w[i], to + i);
+  for (int i = 0; i < N; ++i) {
+    if constexpr (STREAM) __builtin_nontemporal_store(w[i], to + i);
+    else to[i] = w[i];
+  }
+}
+// f(whether to stream) for a condition that is the same in every lane.  (Without
+// the empty statements the compiler would make one plain store of both kinds.)
+template <typename F> __device__ __forceinline__ void streaming(bool stream, F f) {
+  if (stream) {
+    asm volatile("");
+    f(std::true_type());
     asm volatile("");
   } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) to[i] = w[i];
+    f(std::false_type());
   }
 }
 

@@ -461,13 +461,15 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
       }
     }
     __builtin_amdgcn_wave_barrier();
+    streaming(g.stream, [&](auto stream) __attribute__((always_inline)) {
 #pragma unroll
-    for (int c0 = 0; c0 < 32 * OCH; c0 += 64) {
-      const int r = (c0 + lane) / OCH, c = (c0 + lane) % OCH;
-      const int i = i0 + wm * WTM + a * 32 + r, j = j0 + wn * WTN + c * EPC;
-      const uint4 v = mine[r * OPITCH + c];
-      if (i < m_end && j < N) store_whole(reinterpret_cast<uint4*>(O + (size_t)i * N + j), v, g.stream);
-    }
+      for (int c0 = 0; c0 < 32 * OCH; c0 += 64) {
+        const int r = (c0 + lane) / OCH, c = (c0 + lane) % OCH;
+        const int i = i0 + wm * WTM + a * 32 + r, j = j0 + wn * WTN + c * EPC;
+        const uint4 v = mine[r * OPITCH + c];
+        if (i < m_end && j < N) store_whole<stream.value>(reinterpret_cast<uint4*>(O + (size_t)i * N + j), v);
+      }
+    });
     __builtin_amdgcn_wave_barrier();
   }
 }
@@ -610,7 +612,9 @@ __global__ __launch_bounds__(256) void combine_kernel(const CombineArgs g) {
           for (int e = 0; e < 8; ++e) s[e] = fmaf(w[u], f[e], s[e]);
         }
       }
-      store_whole(reinterpret_cast<Raw8<T>*>(g.out) + (size_t)t * vpr + v, pack8(s, T()), g.stream);
+      streaming(g.stream, [&](auto stream) __attribute__((always_inline)) {
+        store_whole<stream.value>(reinterpret_cast<Raw8<T>*>(g.out) + (size_t)t * vpr + v, pack8(s, T()));
+      });
     }
   }
 }
@@ -649,14 +653,16 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const CombineGrad
           }
         }
         if (dy) {
+          streaming(g.stream, [&](auto stream) __attribute__((always_inline)) {
 #pragma unroll
-          for (int u = 0; u < kCombineAhead; ++u) {
-            if (slot[u] < 0) continue;
-            float f[8];
+            for (int u = 0; u < kCombineAhead; ++u) {
+              if (slot[u] < 0) continue;
+              float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = w[u] * d[e];
-            store_whole(dy + (size_t)slot[u] * vpr + v, pack8(f, T()), g.stream);
-          }
+              for (int e = 0; e < 8; ++e) f[e] = w[u] * d[e];
+              store_whole<stream.value>(dy + (size_t)slot[u] * vpr + v, pack8(f, T()));
+            }
+          });
         }
         if (g.dweights) {
 #pragma unroll

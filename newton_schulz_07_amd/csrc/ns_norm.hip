@@ -48,11 +48,11 @@ __device__ __forceinline__ Raw8<T> load8(const T* row, int t, int i, int cols) {
   }
   return r;
 }
-template <typename T, int TPR, int HOW>
-__device__ __forceinline__ void store8(T* row, int t, int i, int cols, const float* f, bool stream) {
+template <typename T, int TPR, int HOW, bool STREAM>
+__device__ __forceinline__ void store8(T* row, int t, int i, int cols, const float* f) {
   const Raw8<T> r = pack8(f, T());
   if (HOW != kSingles) {  // (outputs are contiguous: whole vectors are aligned)
-    if (column<TPR, HOW>(t, i, 0) < cols) store_whole(reinterpret_cast<Raw8<T>*>(row) + t + i * TPR, r, stream);
+    if (column<TPR, HOW>(t, i, 0) < cols) store_whole<STREAM>(reinterpret_cast<Raw8<T>*>(row) + t + i * TPR, r);
   } else {
     T x[8];
     __builtin_memcpy(x, &r, sizeof(r));
@@ -137,14 +137,16 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void layer_norm_kernel(const
     }
     const float rstd = 1.0f / sqrtf(row_sum<WPR>(s, 0.0f, red[1]).x / n + g.eps);
     T* y = reinterpret_cast<T*>(g.y) + row * (long long)g.cols;
+    streaming(g.stream, [&](auto stream) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      float f[8];
-      unpack8(r[i], f);
+      for (int i = 0; i < VPT; ++i) {
+        float f[8];
+        unpack8(r[i], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[i][e], b[i][e]);
-      store8<T, TPR, HOW>(y, t, i, g.cols, f, g.stream);
-    }
+        for (int e = 0; e < 8; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[i][e], b[i][e]);
+        store8<T, TPR, HOW, stream.value>(y, t, i, g.cols, f);
+      }
+    });
     if (t == 0) {
       if (g.mean) g.mean[row] = mean;
       if (g.rstd) g.rstd[row] = rstd;
@@ -186,7 +188,9 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(const LayerNormAr
       unpack8(load8<T, 1024, HOW>(x, t, i, g.cols), f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[0][e], b[0][e]);
-      store8<T, 1024, HOW>(y, t, i, g.cols, f, g.stream);
+      streaming(g.stream, [&](auto stream) __attribute__((always_inline)) {
+        store8<T, 1024, HOW, stream.value>(y, t, i, g.cols, f);
+      });
     }
     if (t == 0) {
       if (g.mean) g.mean[row] = mean;
@@ -251,18 +255,20 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void layer_norm_backward_ker
     c2 = c.y * inv_n;
     if (g.dx) {
       T* dx = reinterpret_cast<T*>(g.dx) + row * (long long)g.cols;
+      streaming(g.stream, [&](auto stream) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        float fx[8], fd[8];
-        unpack8(rx[i], fx);
-        unpack8(rd[i], fd);
+        for (int i = 0; i < VPT; ++i) {
+          float fx[8], fd[8];
+          unpack8(rx[i], fx);
+          unpack8(rd[i], fd);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xh = (fx[e] - mean) * rstd;
-          fx[e] = rstd * (fmaf(fd[e], w[i][e], -c1) - xh * c2);
+          for (int e = 0; e < 8; ++e) {
+            const float xh = (fx[e] - mean) * rstd;
+            fx[e] = rstd * (fmaf(fd[e], w[i][e], -c1) - xh * c2);
+          }
+          store8<T, TPR, HOW, stream.value>(dx, t, i, g.cols, fx);
         }
-        store8<T, TPR, HOW>(dx, t, i, g.cols, fx, g.stream);
-      }
+      });
     }
   }
   if (g.partials == nullptr) return;
@@ -290,7 +296,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void layer_norm_backward_ker
 #pragma unroll
           for (int r = 0; r < RPB - 1; ++r) x[e] += part[r][(i * 8 + e) * TPR + t];
       }
-      store8<float, TPR, HOW>(out + (size_t)h * ld, t, i, g.cols, x, false);
+      store8<float, TPR, HOW, false>(out + (size_t)h * ld, t, i, g.cols, x);
     }
   }
 }
@@ -343,7 +349,9 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_long_kernel(const La
         const float xh = (fx[e] - mean) * rstd;
         fx[e] = rstd * (fmaf(fd[e], w[0][e], -c1) - xh * c2);
       }
-      store8<T, 1024, HOW>(dx, t, i, g.cols, fx, g.stream);
+      streaming(g.stream, [&](auto stream) __attribute__((always_inline)) {
+        store8<T, 1024, HOW, stream.value>(dx, t, i, g.cols, fx);
+      });
     }
   }
 }
