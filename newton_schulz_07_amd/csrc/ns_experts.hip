@@ -16,11 +16,13 @@
 //
 // bf16, 128 experts of 1536 x 2048, rows spread at random (us; TFLOP/s over the
 // rows that there are):
-//   65536 rows  product 495 (833), input gradient 480 (859), weight gradient 535 (771)
-//   16384 rows  product 238, input gradient 206, weight gradient 262
-//   32 rows     product 28 to 36: HBM or the last-level cache, the chosen
+//   65536 rows  product 505 (816), input gradient 480 (859), weight gradient 465 (887)
+//   16384 rows  product 240, input gradient 207, weight gradient 205
+//   32 rows     product 27 to 35: HBM or the last-level cache, the chosen
 //               experts are 179 MB
-//   65536 rows, 16 experts  375 (1100), 422 (977), 370 (1114)
+//   65536 rows, 16 experts  378 (1091), 402 (1026), 362 (1139)
+// (the same inputs again and again; with others between, the last-level cache
+// does not hold dy, and the weight gradient of 65536 rows takes 540)
 // A large square library product reaches 1200 TFLOP/s here.  At 512 rows to an
 // expert the product's tiles of 256 rows are padded by 28 %, the input
 // gradient's of 128 rows by 12 %, and the weight gradient's 16 stages do not
@@ -30,7 +32,7 @@
 // blocks skipped they take the same time to 2 %.  At 16384 rows the weights and
 // the output are 0.9 GB, and HBM bounds all three.
 // fp32 runs on the fp32 MFMA, a sixteenth of the rate: 999 rows of 7 experts of
-// 520 x 264 take 10, 14 and 12 us; one wave's 32 x 32 block over 520 columns of
+// 520 x 264 take 10, 13 and 11 us; one wave's 32 x 32 block over 520 columns of
 // k is 8 us of matrix instructions.
 //
 // The experts' row counts are known on the device only.  The grid holds the
@@ -118,7 +120,8 @@ __device__ __forceinline__ i32x4 uniform(i32x4 r) {
 }
 
 // GATHER: the weight gradient's x is read through rows.  ONCE: the weights are
-// more than the L2s hold, and few rows read each.
+// more than the L2s hold and few rows read each (4 tokens 31 us, 38 without; with
+// more than one row tile to an expert it loses: 512 tokens 234 and 162).
 template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, int MODE, bool GATHER, bool ONCE>
 __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_kernel(const ExpertsArgs g) {
   constexpr bool PNAT = MODE == EXP_WEIGHT_GRAD, QNAT = MODE != EXP_PRODUCT;
@@ -511,9 +514,10 @@ hipError_t launch_tiles(ExpertsArgs g, hipStream_t st) {
 //                      most), 750 rows 51 / 64 (186), 1000 rows 55 / 67;
 //                      128 experts: 128 rows 263 / 238, 256 rows 344 / 347,
 //                      512 rows 495 / 541; 64 experts, 250 rows 178 / 164
-//     weight gradient  4096 rows to each of 16 experts 370 / 415, 512 of 128
-//                      533 / 538, 500 of 32 137 / 132, 128 of 128 268 / 262;
-//                      1000 rows of 8 78 / 65 (384 tiles)
+//     weight gradient  (both with plain stores) 4096 rows to each of 16
+//                      experts 370 / 415, 512 of 128 533 / 538, 500 of 32 137 /
+//                      132, 128 of 128 268 / 262; 1000 rows of 8 78 / 65 (384
+//                      tiles)
 //     input gradient   128 experts: 256 rows 315 / 296, 512 rows 502 / 487; 1000
 //                      rows of 8 experts 76 / 64: never 256 x 256
 //   128 x 256 against 64 x 64   400 rows of 8 experts 37 / 18, 2000 rows 42 / 52
@@ -576,7 +580,7 @@ hipError_t launch_mode(int dtype, const ExpertsArgs& g, hipStream_t st) {
 // out[t] = sum_j weights[t, j] y[slots[t, j]], in fp32, rounded once: TPT
 // threads to a token, each walking its columns 8 at a time; eight rows are on
 // their way before the first is added.  Bound by HBM: 8192 tokens x 8 rows of
-// 2048 bf16 take 83 us (3.6 TB/s; rows of 4 KB at random), 32 tokens 3.4 us.
+// 2048 bf16 take 56 us (5.4 TB/s; rows of 4 KB at random), 32 tokens 3.2 us.
 constexpr int kCombineAhead = 8;
 constexpr int kCombineBlocks = 1 << 20;  // a launch holds fewer than 2^32 threads: more tokens than that go round
 template <typename T, int TPT>
@@ -621,8 +625,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const CombineArgs g) {
 
 // dy[slot] = weight dout[t],  dweights[t, j] = <dout[t], y[slot]> (fp32): a wave
 // to a token, eight choices at a time, so that dout is read once for them.
-// Bound by HBM: 107 us for the same (5.3 TB/s, y from the last-level cache in
-// part).
+// Bound by HBM: 120 us for the same (4.7 TB/s).
 template <typename T>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const CombineGradArgs g) {
   const int lane = threadIdx.x & 63, vpr = g.cols / 8;

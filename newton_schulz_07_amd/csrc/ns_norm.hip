@@ -8,10 +8,10 @@
 // Both passes are bound by HBM: a row is read once, held in registers as it
 // was stored, and every sum is taken in fp32 (the variance from the centred
 // values, in a second pass over the registers).  Results are rounded to their
-// type once.  8192 x 7168 bf16: forward 44 us (5.3 TB/s of what has to be
-// moved), backward 75 us (4.7 TB/s) and 6 us for the parameters' sums; a large
+// type once.  8192 x 7168 bf16: forward 45 us (5.2 TB/s of what has to be
+// moved), backward 67 us (5.2 TB/s) and 6 us for the parameters' sums; a large
 // copy reaches 4.8 TB/s.  A single row of 2048: 3.0 us, a launch's latency.
-// 1003 x 1531 fp32 (rows of odd length): 7.3, 11.9 and 3.9 us, bound by the
+// 1003 x 1531 fp32 (rows of odd length): 6.6, 12.6 and 4.0 us, bound by the
 // instructions of single-column accesses and by latency.
 #include "ns_device.h"
 #include "ns_lanes.h"
