@@ -125,7 +125,7 @@ __device__ __forceinline__ i32x4 uniform(i32x4 r) {
 template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, int MODE, bool GATHER, bool ONCE>
 __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_kernel(const ExpertsArgs g) {
   constexpr bool PNAT = MODE == EXP_WEIGHT_GRAD, QNAT = MODE != EXP_PRODUCT;
-  constexpr int NW = WM * WN, NT = NW * 64;
+  constexpr int NW = WM * WN;
   constexpr int EPC = Elem<T>::kChunk, ES = (int)sizeof(T), BK = CPR * EPC;
   constexpr int WTM = BM / WM, WTN = BN / WN, SM = WTM / 32, SN = WTN / 32;
   constexpr int LP = BM * CPR, LQ = BN * CPR, STAGE = LP + LQ;
