@@ -36,8 +36,12 @@
  *     no partial work is left behind.  Every call returns an ns_status.
  *   - No entry point falls back to another implementation.
  *   - Calls that share a device AND a stream share one library-owned
- *     workspace and are ordered by that stream; calls on different streams
- *     get different workspaces.
+ *     workspace and are ordered by that stream, also calls of several host
+ *     threads: one enqueues all its work before the other's begins.  Calls
+ *     on different streams get different workspaces.
+ *     A captured call keeps the workspace of the stream it was captured on:
+ *     its replays must not overlap in time with calls on that stream, nor
+ *     with replays of other graphs that were captured on it.
  */
 #ifndef NS_HIP_H
 #define NS_HIP_H

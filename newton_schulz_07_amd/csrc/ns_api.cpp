@@ -216,9 +216,10 @@ int check_grouped(int n, const void* const* in, void* const* out, const int64_t*
 int run_stacks(std::vector<Group>& gs, size_t ws_bytes, int ns_steps, float a, float b, float c, hipStream_t st,
                ns::TileChoice* tc, int launches[3], char* given = nullptr) {
   const int dtype = gs[0].p.dtype;
-  char* ws = given;
-  if (ws == nullptr)
-    if (int s = get_workspace(st, ws_bytes, &ws)) return s;
+  ns::Workspace own;  // held to the end of the call's launches
+  if (given == nullptr)
+    if (int s = get_workspace(st, ws_bytes, &own)) return s;
+  char* const ws = given != nullptr ? given : own.ptr;
   if (g_poison.load() && ws_bytes > 0)
     if (int s = check_hip(hipMemsetAsync(ws, 0xFF, ws_bytes, st), "workspace poison fill")) return s;
   std::vector<Plan> plans;
@@ -470,9 +471,9 @@ int ns_stage_normalize(const void* x, void* x0, float* norms, int64_t batch, int
   if (int s = check_arch()) return s;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Plan p = make_plan(batch, rows, cols, dtype);
-  char* ws = nullptr;
+  ns::Workspace ws;
   if (int s = get_workspace(st, p.total, &ws)) return s;
-  return run_normalize(x, x0, norms, p, reinterpret_cast<float*>(ws + p.off_part), st);
+  return run_normalize(x, x0, norms, p, reinterpret_cast<float*>(ws.ptr + p.off_part), st);
 }
 
 int ns_stage_gram(const void* x, void* a_off, float* a_diag, int64_t batch, int64_t rows, int64_t cols,

@@ -77,21 +77,26 @@ namespace {
 struct Ws {
   void* ptr = nullptr;
   size_t bytes = 0;
+  std::mutex enqueueing;  // held from taking the buffer to the last launch that uses it
 };
-std::mutex g_ws_mu;
+std::mutex g_ws_mu;  // the containers below (taken after an `enqueueing`, never before one)
 std::map<std::pair<int, void*>, Ws> g_ws;
 // Buffers replaced by a larger one.  Work queued earlier may still read
-// them, and another thread may hold the pointer between taking it and
-// enqueueing its launches, so they are freed only by ns_release_workspace.
+// them, so they are freed only by ns_release_workspace.
 std::vector<std::pair<int, void*>> g_ws_retired;
 std::atomic<int64_t> g_ws_allocs{0};
 }  // namespace
 
-int get_workspace(hipStream_t st, size_t bytes, char** out) {
+int get_workspace(hipStream_t st, size_t bytes, Workspace* out) {
   int dev = 0;
   if (int s = check_hip(hipGetDevice(&dev), "hipGetDevice")) return s;
-  std::lock_guard<std::mutex> lk(g_ws_mu);
-  Ws& w = g_ws[{dev, (void*)st}];
+  Ws* found = nullptr;
+  {
+    std::lock_guard<std::mutex> lk(g_ws_mu);
+    found = &g_ws[{dev, (void*)st}];  // (stays where it is until ns_release_workspace, which runs beside no call)
+  }
+  Ws& w = *found;
+  std::unique_lock<std::mutex> held(w.enqueueing);
   if (w.bytes < bytes) {
     void* p = nullptr;
     if (hipMalloc(&p, bytes) != hipSuccess || p == nullptr) {
@@ -99,11 +104,15 @@ int get_workspace(hipStream_t st, size_t bytes, char** out) {
       return fail(NS_ERR_OOM, "workspace allocation of " + std::to_string(bytes) + " bytes failed");
     }
     ++g_ws_allocs;
-    if (w.ptr != nullptr) g_ws_retired.emplace_back(dev, w.ptr);
+    if (w.ptr != nullptr) {
+      std::lock_guard<std::mutex> lk(g_ws_mu);
+      g_ws_retired.emplace_back(dev, w.ptr);
+    }
     w.ptr = p;
     w.bytes = bytes;
   }
-  *out = static_cast<char*>(w.ptr);
+  out->ptr = static_cast<char*>(w.ptr);
+  out->held = std::move(held);
   return NS_OK;
 }
 

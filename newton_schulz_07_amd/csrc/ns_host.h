@@ -9,6 +9,7 @@
 
 #include <atomic>
 #include <exception>
+#include <mutex>
 #include <new>
 #include <string>
 
@@ -47,8 +48,15 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb);
 // The workspace of (current device, st), grown to at least `bytes`.  A warm
 // workspace is returned without any HIP call, so calls on a stream that has
 // seen a call of the same or a larger size enqueue only kernels and copies
-// (graph capture needs exactly that).
-int get_workspace(hipStream_t st, size_t bytes, char** out);
+// (graph capture needs exactly that).  It is the calling thread's own while
+// `held` lives: an entry point keeps it until the last launch that uses the
+// workspace is enqueued, so that calls of several threads on one stream are
+// ordered by that stream as a whole, not launch by launch.
+struct Workspace {
+  char* ptr = nullptr;
+  std::unique_lock<std::mutex> held;
+};
+int get_workspace(hipStream_t st, size_t bytes, Workspace* out);
 
 // Timing of one launch of a kind: events that travel in the kernel's dispatch
 // packet (set_launch_events), so timing adds no packets between the kernels

@@ -603,7 +603,9 @@ __device__ __forceinline__ void place_tokens(const RouteArgs& g, int p0, int p1,
     const int slot = place(e, live, g.experts, base, cnt);
     if (live) {
       g.slots[p] = slot;
-      g.rows[slot] = p / g.top_k;
+      // (counts that are another call's, such as those of two graphs that were
+      // captured on one stream and run on two, lead to no write outside rows)
+      if ((unsigned)slot < (unsigned)(g.tokens * g.top_k)) g.rows[slot] = p / g.top_k;
     }
   }
 }

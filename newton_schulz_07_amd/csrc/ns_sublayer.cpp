@@ -187,12 +187,12 @@ int ns_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t 
     hipStream_t st = static_cast<hipStream_t>(stream);
     const int blocks = norm_backward_blocks(rows, (int)cols);
     const size_t bytes = params ? (size_t)blocks * 2 * partials_ld((int)cols) * sizeof(float) : 0;
-    char* ws = nullptr;
+    Workspace ws;  // held to the end of the call's launches
     if (bytes > 0) {
       if (int s = get_workspace(st, bytes, &ws)) return s;
-      if (int s = poison(ws, bytes, st)) return s;
+      if (int s = poison(ws.ptr, bytes, st)) return s;
     }
-    LayerNormGradArgs g{dy, x, weight, mean, rstd, dx, dweight, dbias, reinterpret_cast<float*>(ws),
+    LayerNormGradArgs g{dy, x, weight, mean, rstd, dx, dweight, dbias, reinterpret_cast<float*>(ws.ptr),
                         rows, lddy, ldx, (int)cols, param_dtype};
     if (int s = check_hip(timed_launch(NS_KIND_LAYER_NORM, st,
                                        [&] { return launch_layer_norm_backward(dtype, g, blocks, st); }),
@@ -238,13 +238,13 @@ int ns_route(const void* logits, int64_t ld, const float* bias, int32_t* ids, fl
     if (int s = check_apart(out, in)) return s;
     if (int s = check_arch()) return s;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    char* ws = nullptr;
+    Workspace ws;  // held to the end of the call's launches
     const size_t bytes = route_workspace((int)tokens, (int)experts);
     if (plan && bytes > 0) {
       if (int s = get_workspace(st, bytes, &ws)) return s;
-      if (int s = poison(ws, bytes, st)) return s;
+      if (int s = poison(ws.ptr, bytes, st)) return s;
     }
-    RouteArgs g{logits, bias, ids, weights, offsets, rows, slots, reinterpret_cast<int*>(ws), ld, (int)tokens,
+    RouteArgs g{logits, bias, ids, weights, offsets, rows, slots, reinterpret_cast<int*>(ws.ptr), ld, (int)tokens,
                 (int)experts, (int)top_k, (int)groups, (int)top_groups, group_best, score, renormalize != 0,
                 route_shape((int)tokens, (int)experts).hist_ld, scale};
     if (int s = check_hip(timed_launch(NS_KIND_ROUTE, st, [&] { return launch_route(dtype, g, st); }), "route launch"))
