@@ -321,7 +321,8 @@ int ns_stage_update(const void* x, const void* c_off, const float* c_diag,
  *   - Outputs share no memory with inputs or with each other
  *     (NS_ERR_INVALID_ARG).
  *   - A row's length, and the elements between rows, are at most 2^20, a row
- *     count below 2^31.
+ *     count below 2^31; tokens * top_k of ns_route and n_rows of the experts'
+ *     products are at most 2^31 - 1024.
  *   - Sums are taken in fp32 and every result is rounded once to its type.
  *     No atomics touch a floating-point value: the same inputs give the same
  *     bits.

@@ -12,6 +12,10 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 20;     // columns of a row, and elements between rows
 constexpr int64_t kMaxRows = int64_t(1) << 31;    // row counts stay below
+// Choices of a routing and sorted rows of the experts: kernels step through
+// them in 32-bit numbers, to the end of a block's or a tile's last step, which
+// is up to 1024 past the last one.
+constexpr int64_t kMaxStepped = kMaxRows - 1024;
 constexpr int64_t kMaxTokens = int64_t(1) << 25;  // and routed tokens: a launch holds fewer than 2^32 threads, 64 to a token
 
 int check_rows(int64_t n, const char* name) {
@@ -84,7 +88,7 @@ int check_route(int64_t tokens, int64_t experts, int64_t top_k, int64_t ld, int 
 
 int check_experts(int64_t n_rows, int64_t experts, int64_t fan_out, int64_t fan_in, int dtype) {
   if (int s = check_dtype(dtype)) return s;
-  if (int s = check_rows(n_rows, "n_rows")) return s;
+  if (n_rows < 0 || n_rows > kMaxStepped) return fail(NS_ERR_INVALID_ARG, "n_rows must be in [0, 2^31 - 1024]");
   if (experts < 1 || experts > kMaxExperts)
     return fail(NS_ERR_INVALID_ARG, "experts must be in [1, " + std::to_string(kMaxExperts) + "]");
   if (int s = check_cols(fan_out, "fan_out")) return s;
@@ -210,6 +214,8 @@ int ns_route(const void* logits, int64_t ld, const float* bias, int32_t* ids, fl
              int64_t top_groups, int group_best, int score, int renormalize, float scale, int dtype, void* stream) {
   return entry([&]() -> int {
     if (int s = check_route(tokens, experts, top_k, ld, score, dtype)) return s;
+    if (tokens * top_k > kMaxStepped)
+      return fail(NS_ERR_INVALID_ARG, "tokens * top_k must be at most 2^31 - 1024");
     if (groups < 1 || groups > kMaxGroups || experts % groups != 0)
       return fail(NS_ERR_INVALID_ARG, "groups must be in [1, " + std::to_string(kMaxGroups) + "] and divide experts");
     if (top_groups < 1 || top_groups > groups)
