@@ -243,10 +243,12 @@ __device__ __forceinline__ bool choose(const RouteArgs& g, const T* row, long lo
       __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's LDS writes are done
       __builtin_amdgcn_wave_barrier();
       constexpr int GPL = kMaxGroups / L, GLOW = kMaxGroups - 1;
-      int rank[GPL];
+      int rank[GPL], ranked[GPL];
+      float size[GPL];  // of the keys in a group's rank: each was rounded at its own
 #pragma unroll
       for (int i = 0; i < GPL; ++i) {
-        rank[i] = kClosed;
+        rank[i] = ranked[i] = kClosed;
+        size[i] = 0.0f;
         if (i * L >= g.groups) continue;
         const int h = ll + i * L;
         float a = -INFINITY, b = -INFINITY;
@@ -262,7 +264,9 @@ __device__ __forceinline__ bool choose(const RouteArgs& g, const T* row, long lo
               a = x[u] > a ? x[u] : a;
             }
           }
-          rank[i] = packed<GLOW>(g.group_best > 1 && gs > 1 ? a + b : a, h);
+          const bool two = g.group_best > 1 && gs > 1;
+          rank[i] = ranked[i] = packed<GLOW>(two ? a + b : a, h);
+          size[i] = two ? fabsf(a) + fabsf(b) : 0.0f;
         }
       }
       unsigned kept[2] = {0, 0};
@@ -283,7 +287,17 @@ __device__ __forceinline__ bool choose(const RouteArgs& g, const T* row, long lo
         kept[0] |= h < 32 ? 1u << h : 0u;
         kept[1] |= h < 32 ? 0u : 1u << (h - 32);
       }
-      sure = g.top_groups == g.groups || apart<GLOW>(last, m, 2.0f * off);
+      // A score's error enters a rank twice.  So does half a step of each key,
+      // which is more than the rank's own where biases cancel: up to 2^-24 of
+      // the two sizes, of either group.
+      float blur = 2.0f * off;
+      if (has_bias) {
+        float most_of = 0.0f;
+#pragma unroll
+        for (int i = 0; i < GPL; ++i) most_of = ranked[i] == last || ranked[i] == m ? fmaxf(most_of, size[i]) : most_of;
+        blur += 0x1p-22f * lanes_max<L>(most_of);
+      }
+      sure = g.top_groups == g.groups || apart<GLOW>(last, m, blur);
 #pragma unroll
       for (int v = 0; v < V; ++v) key[v] = (of[v] < 32 ? kept[0] : kept[1]) >> (of[v] & 31) & 1 ? key[v] : kClosed;
     }

@@ -1,0 +1,45 @@
+"""Edge cases of the mixture-of-experts sublayer's operators against the oracle in float64: keys that cancel, masked
+experts with a bias, saturated scores, rows that nothing names, launches at their largest.
+
+Error bounds as in test_gpu_sublayer.py: U = 2^-24; a store to type T is off by at most half a step.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import newton_schulz_07_amd as ns
+from oracle import sublayer as ref
+from tests.gpu_util import device, to64
+from tests.test_gpu_sublayer import DTYPES, U, check_route, half_step, near, normal
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------- routing
+
+
+@pytest.mark.parametrize("tokens", [1500, 4500])  # a wave to a token, and 16 lanes
+@pytest.mark.parametrize("score,shift,scale,by", [
+    ("softmax", 0.0, 0.5, 256.0), ("softmax", 0.0, 0.5, 1024.0),  # scores of about 2^-7: beside 1024 they keep 6 bits
+    ("sigmoid", 0.0, 1.5, 16000.0), ("sigmoid", -10.0, 1.0, 16.0),
+])
+def test_route_ranks_groups_whose_biases_cancel(tokens, score, shift, scale, by):
+    # the two experts of a group have keys near `by` and -`by`: their sum is far below either's rounding; all the
+    # experts of the chosen groups are chosen
+    logits = normal((tokens, 128), 200, scale=scale, shift=shift)
+    bias = torch.tensor([by, -by]).repeat(64)
+    kw = dict(groups=64, top_groups=7, group_best=2, score=score)
+    r = ns.ns_route(logits.to(device()), 14, bias=bias.to(device()), **kw)
+    check_route(logits, (14,), dict(kw, bias=to64(bias)), r)
+
+
+def test_route_ranks_groups_beside_a_closed_one():
+    # a bias that takes a whole group out does not blur the others' ranks
+    logits = normal((4500, 64), 201)
+    bias = normal((64,), 202, scale=0.1)
+    bias[8:16] = -1e9
+    kw = dict(groups=8, top_groups=4, group_best=2, score="sigmoid")
+    r = ns.ns_route(logits.to(device()), 6, bias=bias.to(device()), **kw)
+    check_route(logits, (6,), dict(kw, bias=to64(bias)), r)
+    assert not ((r.ids >= 8) & (r.ids < 16)).any()
