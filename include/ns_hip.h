@@ -371,12 +371,14 @@ enum {
  *   bias      fp32 [experts], or NULL.  It moves the choice, not the weights.
  *   ids       int32 [tokens, top_k]: the experts with the largest keys, in
  *             descending order, equal keys by index.  The key is score + bias,
- *             or with no bias the logit itself.
+ *             or with no bias the logit itself; that of a logit of -inf is
+ *             -inf in both.
  *   groups, top_groups, group_best
  *             the experts form `groups` groups of neighbours, ranked by the
- *             sum of their group_best (1 or 2) largest score + bias (scores
- *             with no bias); only experts of the best top_groups are chosen.
- *             1, 1 for no groups.
+ *             sum of their group_best (1 or 2) largest keys (scores with no
+ *             bias), in which keys of -inf count for nothing; a group of
+ *             nothing else comes last.  Only experts of the best top_groups
+ *             are chosen.  1, 1 for no groups.
  *   weights   fp32 [tokens, top_k]: scale s / (sum of the chosen s + 1e-20)
  *             if renormalize, else scale s; s is the expert's score.
  *   offsets, rows, slots
@@ -387,8 +389,9 @@ enum {
  *             choice j of token t is sorted row slots[t, j] (int32).
  *
  * tokens < 2^25, experts <= 1024, top_k <= 64, groups <= 64 and a divisor of experts.
- * Keys that pass through exp are compared in 64 bits.  A logit of -inf has
- * score 0 and comes last; a row of nothing else has weights 0.  A NaN key
+ * Keys that pass through exp are compared in 64 bits.  A logit of -inf takes
+ * an expert out: it has score 0 and comes after all others of the kept groups,
+ * whatever its bias; a row of nothing else has weights 0.  A NaN key
  * counts as -inf, a NaN score makes the weights it enters NaN; ids are always
  * top_k distinct experts.
  */

@@ -1,9 +1,11 @@
 // ns_route.hip - routing of tokens to experts, and its gradient.
 //
 //   s = softmax or sigmoid of a token's logits
-//   key = s + bias, or the logit itself where there is no bias
-//   groups: a group's rank is the sum of its group_best largest s + bias (s
-//   without a bias); only the experts of the top_groups best groups stay
+//   key = s + bias, or -inf for a logit of -inf; where there is no bias the
+//   logit itself
+//   groups: a group's rank is the sum of its group_best largest keys (s
+//   without a bias), to which -inf adds nothing (-inf for a group of nothing
+//   else); only the experts of the top_groups best groups stay
 //   ids = the top_k largest keys (equal ones: the lower index first)
 //   weights = scale s[ids] / (sum s[ids] + 1e-20), or scale s[ids]
 //
@@ -134,10 +136,10 @@ template <int LOW> __device__ __forceinline__ bool apart(int above, int below, f
 
 // The same of an expert's neighbours in the order of their keys: s + bias, or
 // logits, which are exact but for the bits that the index took (-inf has
-// none).  Nothing after the last expert.
+// none: it goes by the index alone).  Nothing after the last expert.
 template <int LOW> __device__ __forceinline__ bool in_order(int above, int below, bool has_bias, float off) {
-  const bool logits = ((above ^ below) & ~LOW) != 0 || (below & ~LOW) == (kLeast & ~LOW);
-  return below == kClosed || (has_bias ? apart<LOW>(above, below, off) : logits);
+  if (below == kClosed || (below & ~LOW) == (kLeast & ~LOW)) return true;
+  return has_bias ? apart<LOW>(above, below, off) : ((above ^ below) & ~LOW) != 0;
 }
 // The token's lane before this one; `first` in its first.
 template <int L> __device__ __forceinline__ int before(int v, int first) {
@@ -222,7 +224,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& g, const T* row, long lo
     float r[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      r[v] = has_bias ? s[v] + shift[v] : s[v];
+      r[v] = !has_bias ? s[v] : l[v] == -INFINITY ? -INFINITY : s[v] + shift[v];
       key[v] = packed<LOW>(has_bias ? r[v] : l[v], e0 + v);
     }
     if (g.groups > 1) {
@@ -264,7 +266,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& g, const T* row, long lo
               a = x[u] > a ? x[u] : a;
             }
           }
-          const bool two = g.group_best > 1 && gs > 1;
+          const bool two = g.group_best > 1 && gs > 1 && b > -INFINITY;
           rank[i] = ranked[i] = packed<GLOW>(two ? a + b : a, h);
           size[i] = two ? fabsf(a) + fabsf(b) : 0.0f;
         }
@@ -297,7 +299,8 @@ __device__ __forceinline__ bool choose(const RouteArgs& g, const T* row, long lo
         for (int i = 0; i < GPL; ++i) most_of = ranked[i] == last || ranked[i] == m ? fmaxf(most_of, size[i]) : most_of;
         blur += 0x1p-22f * lanes_max<L>(most_of);
       }
-      sure = g.top_groups == g.groups || apart<GLOW>(last, m, blur);
+      const bool least = (m & ~GLOW) == (kLeast & ~GLOW);  // nothing in the group: by its index
+      sure = g.top_groups == g.groups || least || apart<GLOW>(last, m, blur);
 #pragma unroll
       for (int v = 0; v < V; ++v) key[v] = (of[v] < 32 ? kept[0] : kept[1]) >> (of[v] & 31) & 1 ? key[v] : kClosed;
     }
@@ -393,8 +396,8 @@ __device__ __forceinline__ bool choose(const RouteArgs& g, const T* row, long lo
       }
       if (ll < n) {
         const double x = logit(row, LOW - (mine[0] & LOW));
-        exact = softmax ? (x == -INFINITY ? 0.0 : exp(x - (double)top)) / sum : 1.0 / (1.0 + exp(-x));
-        exact += (double)g.bias[LOW - (mine[0] & LOW)];
+        exact = softmax ? exp(x - (double)top) / sum : 1.0 / (1.0 + exp(-x));
+        exact = x == -INFINITY ? -INFINITY : exact + (double)g.bias[LOW - (mine[0] & LOW)];
       }
     } else if (ll < n) {
       exact = logit(row, LOW - (mine[0] & LOW));
@@ -450,7 +453,7 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs& g, const T* row,
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     key[v] = has_bias ? s[v] + (F)(e0 + v < E ? g.bias[e0 + v] : 0.0f) : (F)l[v];
-    if (!(key[v] == key[v])) key[v] = (F)-INFINITY;
+    if (!(key[v] == key[v]) || l[v] == -INFINITY) key[v] = (F)-INFINITY;
   }
   if (g.groups > 1) {
     // lane i ranks groups i, i + L, ...; a group's keys stand an odd number
@@ -477,7 +480,7 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs& g, const T* row,
           b = fmax(b, fmin(a, r));
           a = fmax(a, r);
         }
-      rank[i] = g.group_best > 1 && gs > 1 ? a + b : a;
+      rank[i] = g.group_best > 1 && gs > 1 && b > -INFINITY ? a + b : a;
       if (!(rank[i] == rank[i])) rank[i] = -INFINITY;
       if (grp >= g.groups) rank[i] = NAN;  // NaN: not to be chosen (any more)
     }

@@ -172,11 +172,12 @@ def ns_route(logits, top_k, bias=None, groups=1, top_groups=1, group_best=2, sco
              scale=1.0, plan=True):
     """Chooses top_k experts for each token: a Routing.
 
-    logits: [..., experts] fp32 or bf16.  bias: fp32 [experts], moves the
-    choice only.  groups, top_groups, group_best: only experts of the best
-    top_groups of `groups` groups of neighbours, ranked by their group_best
-    largest scores.  score: "softmax" or "sigmoid".  plan=False: no offsets,
-    rows and slots.
+    logits: [..., experts] fp32 or bf16; -inf takes an expert out (it comes
+    last, with weight 0).  bias: fp32 [experts], moves the choice only.
+    groups, top_groups, group_best: only experts of the best top_groups of
+    `groups` groups of neighbours, ranked by their group_best largest scores
+    (with the bias; experts taken out add nothing).  score: "softmax" or
+    "sigmoid".  plan=False: no offsets, rows and slots.
     """
     tokens, experts, ld = _rows_of(logits, "logits")
     code = _score(score)

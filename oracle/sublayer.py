@@ -42,7 +42,7 @@ def route(logits, top_k, bias=None, groups=1, top_groups=1, group_best=2, score=
     z = np.asarray(logits, np.float64)
     T, E = z.shape
     s = scores(z, score)
-    keys = z.copy() if bias is None else s + np.asarray(bias, np.float64)
+    keys = z.copy() if bias is None else np.where(z == -np.inf, -np.inf, s + np.asarray(bias, np.float64))
     ranks = s if bias is None else keys
     keys = np.where(np.isnan(keys), -np.inf, keys)
     ids = np.zeros((T, top_k), np.int64)
@@ -51,8 +51,9 @@ def route(logits, top_k, bias=None, groups=1, top_groups=1, group_best=2, score=
         if groups > 1:
             n = E // groups
             r = np.where(np.isnan(ranks[t]), -np.inf, ranks[t]).reshape(groups, n)
-            best = np.sort(r, axis=1)[:, ::-1][:, :group_best].sum(axis=1)
-            best = np.where(np.isnan(best), -np.inf, best)
+            best = np.sort(r, axis=1)[:, ::-1][:, :group_best]
+            none = best[:, 0] == -np.inf  # keys of -inf add nothing, and a group of nothing else comes last
+            best = np.where(none, -np.inf, np.where(best == -np.inf, 0.0, best).sum(axis=1))
             kept = sorted(range(groups), key=lambda i: (-best[i], i))[:top_groups]
             allowed = np.array([e for e in range(E) if e // n in kept])
         ids[t] = sorted(allowed, key=lambda e: (-keys[t, e], e))[:top_k]

@@ -43,3 +43,41 @@ def test_route_ranks_groups_beside_a_closed_one():
     r = ns.ns_route(logits.to(device()), 6, bias=bias.to(device()), **kw)
     check_route(logits, (6,), dict(kw, bias=to64(bias)), r)
     assert not ((r.ids >= 8) & (r.ids < 16)).any()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("copies", [1, 800])  # a wave to a token, and 16 lanes
+def test_route_masked_experts_come_last_with_a_bias(score, dtype, copies):
+    inf = float("inf")
+    logits = torch.tensor([[0.0, -1.0, -inf, -2.0], [-inf, -inf, 3.0, -inf], [-inf] * 4, [-inf, 1.0, -inf, 1.0],
+                           [1.0, -inf, 0.5, 2.0], [-3.0, 0.0, -1.0, -inf]]).to(dtype).repeat(copies, 1)
+    bias = torch.tensor([0.0, 0.0, 0.9, 0.0])
+    want = torch.tensor([[0, 1, 3, 2], [2, 0, 1, 3], [0, 1, 2, 3], [1, 3, 0, 2], [2, 3, 0, 1], [2, 1, 0, 3]])
+    dev = device()
+    for k in (1, 2, 4):
+        r = ns.ns_route(logits.to(dev), k, bias=bias.to(dev), score=score)
+        if score == "sigmoid":  # (softmax scores of the last rows order differently: the oracle's below)
+            assert torch.equal(r.ids.cpu().long(), want[:, :k].repeat(copies, 1))
+        check_route(logits, (k,), dict(score=score, bias=to64(bias)), r)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_best", [1, 2])
+@pytest.mark.parametrize("tokens", [300, 4500])
+@pytest.mark.parametrize("experts,groups", [(12, 6), (24, 6), (96, 8)])
+def test_route_masked_experts_in_groups_with_a_bias(score, group_best, tokens, experts, groups):
+    # masked ones add nothing to a group's rank; a group of nothing else comes last, whatever its biases are
+    logits = normal((tokens, experts), 203 + experts)
+    gone = torch.rand(tokens, experts, generator=torch.Generator().manual_seed(204)) < 0.5
+    gone[::3, :experts // groups] = True
+    gone[7::50] = True
+    logits[gone] = -float("inf")
+    bias = normal((experts,), 205, scale=0.3)
+    bias[:experts // groups] = 5.0
+    kw = dict(groups=groups, top_groups=groups // 2, group_best=group_best, score=score)
+    r = ns.ns_route(logits.to(device()), 4, bias=bias.to(device()), **kw)
+    check_route(logits, (4,), dict(kw, bias=to64(bias)), r)
+    some = ~gone.view(tokens, groups, -1).all(2)  # groups with an expert left
+    best = r.ids[:, 0].cpu().long()
+    assert some.gather(1, (best // (experts // groups))[:, None])[some.any(1)].all()
