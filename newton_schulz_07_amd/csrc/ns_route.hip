@@ -764,6 +764,8 @@ __global__ __launch_bounds__(1024) void route_place_kernel(const RouteArgs g, in
 // dlogits of a token by one wave.  With p_j = s_j / (sum + 1e-20), or s_j:
 //   ds_j = scale (dw_j - sum_i dw_i p_i) / (sum + 1e-20), or scale dw_j
 //   sigmoid: dl_e = ds_e s_e (1 - s_e);  softmax: dl_e = s_e (ds_e - sum_j ds_j s_j)
+// A sigmoid and its complement both come from e = exp(-|l|), as 1 / (1 + e) and
+// e / (1 + e): of a large logit, which is what is chosen, 1 - s has no bits left.
 // dw is spread over the experts in LDS.  A wave to each token at any length
 // (16384 x 256: 10.9 us, with 16 lanes 16.3), near what HBM takes for 34 MB
 // (7 us).
@@ -792,7 +794,17 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's LDS writes are done
   __builtin_amdgcn_wave_barrier();
-  scores<L, V, float>(l, g.score, s);
+  float rest[V];  // sigmoid: 1 - s
+  if (g.score == NS_SCORE_SIGMOID) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float e = exp_of(-fabsf(l[v])), r = inverse(1.0f + e);
+      s[v] = l[v] < 0.0f ? e * r : r;
+      rest[v] = l[v] < 0.0f ? r : e * r;
+    }
+  } else {
+    scores<L, V, float>(l, g.score, s);
+  }
   bool on[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -823,7 +835,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs
   } x;
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    x.e[v] = (T)(g.score == NS_SCORE_SOFTMAX ? s[v] * (d[v] - mean) : d[v] * s[v] * (1.0f - s[v]));
+    x.e[v] = (T)(g.score == NS_SCORE_SOFTMAX ? s[v] * (d[v] - mean) : d[v] * s[v] * rest[v]);
   if (g.vec_out) {
     if (e0 < E) *reinterpret_cast<Some*>(out) = x;
     return;

@@ -79,7 +79,10 @@ def route_backward(logits, ids, dweights, score="softmax", renormalize=True, sca
             d = (d - (d * sj).sum() / total) / total
         ds = np.zeros(s.shape[1])
         ds[ids[t]] = d
-        out[t] = ds * s[t] * (1 - s[t]) if score == "sigmoid" else s[t] * (ds - (ds * s[t]).sum())
+        if score == "sigmoid":
+            out[t] = ds * s[t] * scores(-logits[t:t + 1], score)[0]  # (1 - s has no bits left of a large logit)
+        else:
+            out[t] = s[t] * (ds - (ds * s[t]).sum())
     return out
 
 

@@ -81,3 +81,35 @@ def test_route_masked_experts_in_groups_with_a_bias(score, group_best, tokens, e
     some = ~gone.view(tokens, groups, -1).all(2)  # groups with an expert left
     best = r.ids[:, 0].cpu().long()
     assert some.gather(1, (best // (experts // groups))[:, None])[some.any(1)].all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_backward_of_saturated_sigmoids(dtype, renorm):
+    # 1 - s from the logit: the gradient of the chosen, highest logits keeps its bits
+    T, E, k = 130, 40, 6
+    logits = normal((T, E), 206, dtype, 1.0)
+    for t in range(T):  # logits from 8 to 40 and from -8 to -40 among the others, alone in some rows
+        g = torch.Generator().manual_seed(1000 + t)
+        far = (8 + 32 * torch.rand(E, generator=g)) * (1 if t % 2 else -1)
+        at = torch.randperm(E, generator=g)[:E if t % 5 == 0 else 5]
+        logits[t, at] = far[at].to(dtype)
+    dev = device()
+    ids = ns.ns_route(logits.to(dev), k, score="sigmoid").ids
+    d = normal((T, k), 207)
+    got = ns.ns_route_backward(logits.to(dev), ids, d.to(dev), score="sigmoid", renormalize=renorm, scale=1.5)
+    L, I, D = to64(logits), ids.cpu().numpy(), to64(d)
+    s, c = 1 / (1 + np.exp(-L)), 1 / (1 + np.exp(L))
+    sj = np.take_along_axis(s, I, 1)
+    mag = 1.5 * np.abs(D)
+    ds = 1.5 * D
+    if renorm:
+        tot = sj.sum(1, keepdims=True) + 1e-20
+        ds = (ds - (ds * sj).sum(1, keepdims=True) / tot) / tot
+        mag = (mag + (mag * sj).sum(1, keepdims=True) / tot) / tot
+    want, full = np.zeros_like(s), np.zeros_like(s)
+    np.put_along_axis(want, I, ds, 1)
+    np.put_along_axis(full, I, mag, 1)
+    want, into = want * s * c, full * s * c
+    near(to64(torch.from_numpy(ref.route_backward(L, I, D, "sigmoid", renorm, 1.5))), want, 1e-13 * into)
+    near(got, want, half_step(dtype) * np.abs(want) + (64 + E / 8) * U * into + 1e-38)

@@ -24,3 +24,11 @@ def test_masked_experts_add_nothing_to_a_group():
     assert ref.route(z, 1, top_groups=1, **kw)[0].tolist() == [[2]]
     assert ref.route(z, 3, top_groups=2, **kw)[0].tolist() == [[2, 4, 5]]
     assert ref.route(z, 2, top_groups=1, **kw)[0].tolist() == [[2, 3]]
+
+
+def test_the_gradient_of_saturated_sigmoids():
+    # s (1 - s) = e / (1 + e)^2 with e = exp(-|l|)
+    z = np.concatenate([np.linspace(8, 60, 14), np.linspace(-8, -60, 14)])[None]
+    e = np.exp(-np.abs(z[0]))
+    got = ref.route_backward(z, np.arange(28)[None], np.ones((1, 28)), "sigmoid", False, 2.0)[0]
+    assert np.all(np.abs(got - 2 * e / (1 + e) ** 2) <= 1e-14 * got)
