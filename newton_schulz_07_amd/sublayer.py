@@ -230,7 +230,8 @@ def ns_experts_product(x, w, offsets, rows=None, y=None):
 
     x: [n_x, fan_in]; w: [experts, fan_out, fan_in]; offsets, rows: int32,
     from ns_route (rows None: x is sorted already).  Returns y [n_rows,
-    fan_out].
+    fan_out]; rows that no expert has (offsets that end below n_rows) are not
+    written.
     """
     experts, fan_out, w_in = _dense(w, "w", x, x.dtype).shape
     n_x, fan_in, ld, n_rows = _sorted_rows(x, rows, experts, offsets)
@@ -243,8 +244,8 @@ def ns_experts_product(x, w, offsets, rows=None, y=None):
 
 
 def ns_experts_input_grad(dy, w, offsets, dx=None):
-    """dx[i] = dy[i] @ w[e] for the sorted rows: [n_rows, fan_in].  ns_experts_combine(dx, slots) adds them up to
-    the gradient of x."""
+    """dx[i] = dy[i] @ w[e] for the sorted rows: [n_rows, fan_in], rows that no expert has not written.
+    ns_experts_combine(dx, slots) adds them up to the gradient of x."""
     experts, fan_out, fan_in = _dense(w, "w", dy, dy.dtype).shape
     n_rows = dy.shape[0]
     _dense(dy, "dy", w, None, (n_rows, fan_out))
@@ -298,13 +299,19 @@ def ns_experts_combine(y, slots, weights=None, out=None):
 
 
 def ns_experts_combine_backward(dout, y, slots, weights=None, dy=None, dweights=None):
-    """(dy, dweights) of ns_experts_combine; dweights is None without weights."""
+    """(dy, dweights) of ns_experts_combine; dweights is None without weights.
+
+    No two slots may be the same.  Rows of y that are more than there are slots have a gradient of zero; where there
+    are as many slots as rows, but some out of range, the rows that none names are not written: pass a dy of zeros.
+    """
     if y.dim() != 2:
         raise ValueError("y must be [n_rows, cols]")
     _dense(y, "y")
     tokens, top_k = _slots_of(slots, weights, y)
     n_rows, cols = y.shape
     _dense(dout, "dout", y, y.dtype, (*slots.shape[:-1], cols))
+    if dy is None and tokens * top_k != n_rows:
+        dy = torch.zeros_like(y)  # rows that no slot names are not written
     dy = _out_like(dy, "dy", y)
     if weights is not None:
         dweights = _out_like(dweights, "dweights", weights)

@@ -113,3 +113,27 @@ def test_route_backward_of_saturated_sigmoids(dtype, renorm):
     want, into = want * s * c, full * s * c
     near(to64(torch.from_numpy(ref.route_backward(L, I, D, "sigmoid", renorm, 1.5))), want, 1e-13 * into)
     near(got, want, half_step(dtype) * np.abs(want) + (64 + E / 8) * U * into + 1e-38)
+
+
+# --------------------------------------------------------------- combine
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens", [0, 1, 40])
+def test_combine_backward_gives_spare_rows_no_gradient(dtype, tokens):
+    # more rows of y than choices: the rows that no choice names have a gradient of zero
+    dev, rows, cols = device(), 200, 136
+    slots = torch.randperm(rows, generator=torch.Generator().manual_seed(208))[:3 * tokens].int().view(tokens, 3)
+    y, dout, w = normal((rows, cols), 209, dtype), normal((tokens, cols), 210, dtype), normal((tokens, 3), 211)
+    torch.cuda.empty_cache()
+    held = torch.full((rows, cols), float("nan"), dtype=dtype, device=dev)  # what a buffer taken next would hold
+    del held
+    want, _ = ref.combine_backward(to64(dout), to64(y), slots.numpy(), to64(w))
+    for weights in (w, None):
+        if weights is None:
+            want, _ = ref.combine_backward(to64(dout), to64(y), slots.numpy())
+        dy, _ = ns.ns_experts_combine_backward(dout.to(dev), y.to(dev), slots.to(dev),
+                                               None if weights is None else weights.to(dev))
+        near(dy, want, (half_step(dtype) + 2 * U) * np.abs(want))
+        held = torch.full_like(dy, float("nan"))
+        del held, dy
