@@ -582,7 +582,6 @@ hipError_t launch_mode(int dtype, const ExpertsArgs& g, hipStream_t st) {
 // their way before the first is added.  Bound by HBM: 8192 tokens x 8 rows of
 // 2048 bf16 take 56 us (5.4 TB/s; rows of 4 KB at random), 32 tokens 3.2 us.
 constexpr int kCombineAhead = 8;
-constexpr int kCombineBlocks = 1 << 20;  // a launch holds fewer than 2^32 threads: more tokens than that go round
 template <typename T, int TPT>
 __global__ __launch_bounds__(256) void combine_kernel(const CombineArgs g) {
   const int vpr = g.cols / 8;
@@ -713,9 +712,13 @@ const char* experts_config(int dtype, ExpertsMode mode, const ExpertsArgs& g) {
 #undef NS_TEXT
 }
 
+// Blocks of so many tokens each: a launch holds fewer than 2^32 threads, more tokens than that go round.
+static unsigned combine_blocks(long long tokens, int per_block) {
+  return (unsigned)std::min(1ll << 20, (tokens + per_block - 1) / per_block);
+}
 template <int TPT>
 static void launch_combine_of(int dtype, const CombineArgs& g, int pieces, hipStream_t st) {
-  const dim3 grid((unsigned)std::min(kCombineBlocks, (g.tokens + 256 / TPT - 1) / (256 / TPT)), (unsigned)pieces);
+  const dim3 grid(combine_blocks(g.tokens, 256 / TPT), (unsigned)pieces);
   if (dtype == 1) dispatch(combine_kernel<bf16, TPT>, grid, dim3(256), st, g);
   else dispatch(combine_kernel<float, TPT>, grid, dim3(256), st, g);
 }
@@ -736,7 +739,7 @@ hipError_t launch_combine(int dtype, const CombineArgs& args, hipStream_t st) {
 hipError_t launch_combine_backward(int dtype, const CombineGradArgs& args, hipStream_t st) {
   CombineGradArgs g = args;
   g.stream = beyond_l2((long long)g.n_rows * g.cols * (dtype == 1 ? 2 : 4));
-  const dim3 grid((unsigned)std::min(kCombineBlocks, (g.tokens + 3) / 4));
+  const dim3 grid(combine_blocks(g.tokens, 4));
   if (dtype == 1) dispatch(combine_backward_kernel<bf16>, grid, dim3(256), st, g);
   else dispatch(combine_backward_kernel<float>, grid, dim3(256), st, g);
   return hipGetLastError();

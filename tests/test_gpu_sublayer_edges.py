@@ -137,3 +137,22 @@ def test_combine_backward_gives_spare_rows_no_gradient(dtype, tokens):
         near(dy, want, (half_step(dtype) + 2 * U) * np.abs(want))
         held = torch.full_like(dy, float("nan"))
         del held, dy
+
+
+def test_combine_of_the_most_tokens():
+    # 2^31 - 1 tokens: counts of blocks past 32 bits
+    T, cols, dev = (1 << 31) - 1, 8, device()
+    y = normal((16, cols), 213, torch.bfloat16).to(dev)
+    slots = torch.arange(16, device=dev, dtype=torch.int32).repeat(1 << 27)[:T].view(T, 1)
+    out = ns.ns_experts_combine(y, slots)
+    at = torch.cat([torch.arange(0, T, 16777259), torch.arange(T - 40, T)]).to(dev)
+    assert torch.equal(out[at], y[at % 16])
+    dw = torch.empty(T, 1, device=dev)
+    status = ns.lib().ns_experts_combine_backward(  # no dy: choices share rows of y
+        out.data_ptr(), y.data_ptr(), slots.data_ptr(), None, None, dw.data_ptr(), T, 1, 16, cols, ns.NS_DTYPE_BF16,
+        torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    norms = (y.double() ** 2).sum(1)
+    near(dw[at, 0], to64(norms[at % 16]), to64(norms[at % 16]) * cols * U)
+    del out, dw, slots
+    torch.cuda.empty_cache()
