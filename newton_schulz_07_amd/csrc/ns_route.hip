@@ -294,10 +294,13 @@ __device__ __forceinline__ bool choose(const RouteArgs& g, const T* row, long lo
       // the two sizes, of either group.
       float blur = 2.0f * off;
       if (has_bias) {
-        float most_of = 0.0f;
+        // (sizes are not negative: their bits are in their order)
+        int most_of = ranked[0] == last || ranked[0] == m ? __float_as_int(size[0]) : 0;
+        if (g.groups > L)
 #pragma unroll
-        for (int i = 0; i < GPL; ++i) most_of = ranked[i] == last || ranked[i] == m ? fmaxf(most_of, size[i]) : most_of;
-        blur += 0x1p-22f * lanes_max<L>(most_of);
+          for (int i = 1; i < GPL; ++i)
+            if (ranked[i] == last || ranked[i] == m) most_of = max(most_of, __float_as_int(size[i]));
+        blur += 0x1p-22f * __int_as_float(lanes_max<L>(most_of));
       }
       const bool least = (m & ~GLOW) == (kLeast & ~GLOW);  // nothing in the group: by its index
       sure = g.top_groups == g.groups || least || apart<GLOW>(last, m, blur);
