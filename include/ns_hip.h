@@ -194,7 +194,8 @@ size_t ns_workspace_bytes_grouped(int n_groups, const int64_t* batch,
 
 /* Free every cached workspace (all devices and streams), replaced ones
  * included.  Synchronises each device that held one.  Must not run while
- * another thread is inside a call.  Returns NS_OK or NS_ERR_HIP. */
+ * another thread is inside a call; graphs that were captured before hold
+ * what it frees and must not be replayed after.  Returns NS_OK or NS_ERR_HIP. */
 int ns_release_workspace(void);
 
 /* Number of workspace allocations (hipMalloc) the library has made since it
@@ -403,8 +404,8 @@ int ns_route(const void* logits, int64_t ld, const float* bias, int32_t* ids,
 
 /*
  * ns_route_backward - dlogits [tokens, experts] dtype from dweights fp32
- * [tokens, top_k], for the choice ids (which has no gradient).  An id outside
- * [0, experts) is left out.
+ * [tokens, top_k], for the choice ids (which has no gradient).  A token's ids
+ * are distinct; one outside [0, experts) is left out.
  */
 int ns_route_backward(const void* logits, int64_t ld, const int32_t* ids,
                       const float* dweights, void* dlogits, int64_t tokens,

@@ -14,23 +14,29 @@
 //                    gathered): k runs over the expert's rows
 // Sums are in fp32 and rounded once.
 //
-// bf16, 128 experts of 1536 x 2048, rows spread at random (us; TFLOP/s over the
-// rows that there are):
-//   65536 rows  product 505 (816), input gradient 480 (859), weight gradient 465 (887)
-//   16384 rows  product 240, input gradient 207, weight gradient 205
-//   32 rows     product 27 to 35: HBM or the last-level cache, the chosen
-//               experts are 179 MB
-//   65536 rows, 16 experts  378 (1091), 402 (1026), 362 (1139)
-// (the same inputs again and again; with others between, the last-level cache
-// does not hold dy, and the weight gradient of 65536 rows takes 540)
-// A large square library product reaches 1200 TFLOP/s here.  At 512 rows to an
-// expert the product's tiles of 256 rows are padded by 28 %, the input
-// gradient's of 128 rows by 12 %, and the weight gradient's 16 stages do not
-// cover a tile's first loads and its stores.  The stages themselves are bound
-// by the path from the L2 to the LDS (16 to 27 bytes a clock and CU; the matrix
-// cores are busy 53 to 58 % of the time): with more stages in flight or dead
-// blocks skipped they take the same time to 2 %.  At 16384 rows the weights and
-// the output are 0.9 GB, and HBM bounds all three.
+// bf16, 128 experts of 1536 x 2048, rows spread at random: us with 1 GiB read
+// between calls (TFLOP/s over the rows that there are), and the same call again
+// and again, which finds part of its inputs in the last-level cache but runs at
+// a lower clock:
+//                           product          input gradient   weight gradient
+//   65536 rows              483 (853), 527   440 (938), 473   489 (843), 456
+//     rows sorted already   471 (875), 499                    478 (862), 499
+//     half of them to one   534 (772), 595   477 (864), 516   781 (528), 670
+//   16384 rows              210, 217         192, 197         234, 198
+//   32 rows                 29, 27           31, 27           134, 136
+//   65536 rows, 16 experts  363 (1137), 363  385 (1070), 395  356 (1159), 353
+// A large square library product reaches 1200 TFLOP/s here.  With 4096 rows to
+// an expert the matrix cores are busy 55 to 59 % of the time, at the 1.8 to 1.9
+// GHz of such loads, and 53 % with 512 rows, where the product's tiles of 256
+// rows are padded by 28 % and the input gradient's of 128 rows by 12 % (their
+// tiles run at 1090 and 1050 TFLOP/s: the padding is what is lost), and the
+// weight gradient's 16 stages do not cover a tile's first loads and its stores.
+// More stages in flight, or dead blocks skipped, change that by 2 % at most.
+// The weight gradient gives an output tile to one workgroup for all of the
+// expert's rows, so an expert that has most of them is a tail of few
+// workgroups.  At 16384 rows the weights and the output are 0.9 GB, and HBM
+// bounds all three; at 32 rows the chosen experts' weights (179 MB) and the
+// weight gradient's 805 MB of output do.
 // fp32 runs on the fp32 MFMA, a sixteenth of the rate: 999 rows of 7 experts of
 // 520 x 264 take 10, 13 and 11 us; one wave's 32 x 32 block over 520 columns of
 // k is 8 us of matrix instructions.
@@ -508,7 +514,8 @@ hipError_t launch_tiles(ExpertsArgs g, hipStream_t st) {
 
 // Tiles of a launch: BM, BN, waves, 16-byte chunks of k, stages, workgroups
 // per CU.  A large tile reads less for each product; a small one pads less and
-// makes more workgroups.  us, 1536 x 2048, bf16 if not said:
+// makes more workgroups.  The rules go by rows and tiles; they were found with
+// experts of 1536 x 2048, and no other shape is measured.  us, bf16 if not said:
 //   256 x 256 against 128 x 256
 //     product          500 rows to each of 8 experts 49 / 37 (138 tiles at
 //                      most), 750 rows 51 / 64 (186), 1000 rows 55 / 67;
@@ -580,7 +587,8 @@ hipError_t launch_mode(int dtype, const ExpertsArgs& g, hipStream_t st) {
 // out[t] = sum_j weights[t, j] y[slots[t, j]], in fp32, rounded once: TPT
 // threads to a token, each walking its columns 8 at a time; eight rows are on
 // their way before the first is added.  Bound by HBM: 8192 tokens x 8 rows of
-// 2048 bf16 take 56 us (5.4 TB/s; rows of 4 KB at random), 32 tokens 3.2 us.
+// 2048 bf16 take 57 us (5.3 TB/s; rows of 4 KB at random), 47 with part of y
+// still in the last-level cache; 32 tokens 3.0 us.
 constexpr int kCombineAhead = 8;
 template <typename T, int TPT>
 __global__ __launch_bounds__(256) void combine_kernel(const CombineArgs g) {
@@ -624,7 +632,9 @@ __global__ __launch_bounds__(256) void combine_kernel(const CombineArgs g) {
 
 // dy[slot] = weight dout[t],  dweights[t, j] = <dout[t], y[slot]> (fp32): a wave
 // to a token, eight choices at a time, so that dout is read once for them.
-// Bound by HBM: 120 us for the same (4.7 TB/s).
+// Bound by HBM: 111 to 129 us for the same (4.4 to 5.1 TB/s).  32 tokens take 8
+// us (fp32 12): a wave walks its token's columns in turn, and there are no more
+// waves.
 template <typename T>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const CombineGradArgs g) {
   const int lane = threadIdx.x & 63, vpr = g.cols / 8;

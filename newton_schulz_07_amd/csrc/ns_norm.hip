@@ -10,7 +10,8 @@
 // values, in a second pass over the registers).  Results are rounded to their
 // type once.  8192 x 7168 bf16: forward 45 us (5.2 TB/s of what has to be
 // moved), backward 67 us (5.2 TB/s) and 6 us for the parameters' sums; a large
-// copy reaches 4.8 TB/s.  A single row of 2048: 3.0 us, a launch's latency.
+// copy reaches 4.8 TB/s.  The backward pass of more than 16384 columns
+// does not fit the registers (norm_shape).  A single row of 2048: 3.0 us, a launch's latency.
 // 1003 x 1531 fp32 (rows of odd length): 6.6, 12.6 and 4.0 us, bound by the
 // instructions of single-column accesses and by latency.
 #include "ns_device.h"

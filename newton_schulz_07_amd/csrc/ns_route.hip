@@ -18,13 +18,20 @@
 // rounding of exp.  A token is first chosen for in fp32, with keys that hold
 // their index in their last bits; where two keys (or two groups' ranks) that
 // decide stand closer than that can tell apart, it is chosen for again in 64
-// bits.  Logits without a bias are compared as they are.
+// bits.  Logits without a bias are compared as they are.  Weights are made in
+// fp32, from scores within a few steps (6e-8 of themselves off in a batch,
+// against 3e-8 if everything but the last rounding is in 64 bits): the experts'
+// outputs that they weigh are bf16 or fp32 sums.  Tokens that are chosen for
+// again have theirs in 64 bits, as a by-product.
 //
 // Bound by instructions and, in small calls, by latency: the logits of 16384
 // tokens and 128 experts are 8 MB (1.8 us of HBM).  16384 x 128 fp32, sigmoid
 // with bias, 4 of 8 groups, top 8: 17 us and 7 us for the plan (with a wave to
 // each token 34 us; with every key in 64 bits as well 65 us).  8192 x 128 softmax, top 8: 6
-// and 7 us, its gradient 5 us.  One token: 4.3 us, of which a launch is 2.5.
+// and 7 us, its gradient 6 us.  One token: 4.3 us, of which a launch is 2.5.
+// Batches of 513 to 1024 experts spill 70 registers, but for bf16 logits
+// without a bias or groups (8192 x 1024, sigmoid: 12 us bf16, 18 fp32, with a
+// bias 28 and 30).
 #include <algorithm>
 #include <type_traits>
 
@@ -769,9 +776,10 @@ __global__ __launch_bounds__(1024) void route_place_kernel(const RouteArgs g, in
 //   sigmoid: dl_e = ds_e s_e (1 - s_e);  softmax: dl_e = s_e (ds_e - sum_j ds_j s_j)
 // A sigmoid and its complement both come from e = exp(-|l|), as 1 / (1 + e) and
 // e / (1 + e): of a large logit, which is what is chosen, 1 - s has no bits left.
-// dw is spread over the experts in LDS.  A wave to each token at any length
-// (16384 x 256: 10.9 us, with 16 lanes 16.3), near what HBM takes for 34 MB
-// (7 us).
+// dw is spread over the experts in LDS; the ids of a token are distinct.  A
+// wave to each token at any length (16384 x 256 fp32, softmax: 11 us, with 16
+// lanes 16.3; sigmoid 10).  HBM would take 7 us for these 34 MB; what takes the
+// rest is not measured.
 template <typename T, int V>
 __global__ __launch_bounds__(256) void route_backward_kernel(const RouteGradArgs g) {
   constexpr int L = 64;

@@ -16,7 +16,9 @@ namespace ns {
 // then leave them at once (store_whole): layer norm and gradient of 8192 x 7168
 // bf16 111 us, 123 without; combine's gradient of 8192 x 8 rows of 2048 and its
 // forward pass 175 and 189; the weight gradient of 128 x 1536 x 2048 from 65536
-// rows 452 and 532, from 16384 rows 201 and 262, from 32 rows 138 and 136.
+// rows 452 and 532, from 16384 rows 201 and 262, from 32 rows 138 and 136 (the
+// same inputs again and again: what an output no longer displaces is then what
+// the next call reads).
 inline bool beyond_l2(long long bytes) { return bytes > (32ll << 20); }
 
 // ------------------------------------------------------------ layer norm
@@ -55,7 +57,11 @@ struct LayerNormGradArgs {
 //   8192 x 7168   256 x 4    38 / 79    1024 x 1  51 / 84
 //   2048 x 12288  1024 x 2   24 / 40    1024 x 4  37 / 270, 1024 x 0  29 / 245
 //   1024 x 32768  1024 x 4   33 / 196   1024 x 0  37 / 316
-// (1024 x 4 spills in the backward pass, and still beats reading rows again.)
+// 1024 x 4 spills 226 to 303 registers in the backward pass, and still beats
+// reading rows again.  Rows of no whole vectors need more of them: 1024 x 4
+// spills 154 to 166 forward too, 1024 x 2 22 to 31 backward:
+//   2048 x 12287  1024 x 2   46 / 74    (fp32 47 / 100)
+//   1024 x 32767  1024 x 4   96 / 426   (fp32 130 / 358)
 struct NormShape {
   int tpr, vpt;
 };
@@ -103,7 +109,8 @@ constexpr int kRouteLeastWaves = 8, kRouteWaves = 16;  // waves of a routing blo
 // blocks.  16384 x 256 (256 blocks) 20.2 us without a scan, 22.3 with one;
 // 8192 x 512 (512 blocks) 42 and 33 us.
 constexpr int kRouteUnscannedBlocks = 256;
-// of the one block that few tokens take (with more than 256 experts 16 would spill registers)
+// of the one block that few tokens take: with more than 256 experts 8 waves, which leave a thread 256 registers
+// (with more than 512, and a bias or groups, it needs 52 more: 8 x 1024 12 us, by logits 5 to 7)
 constexpr int route_single_waves(int experts) { return experts > 256 ? kRouteWaves / 2 : kRouteWaves; }
 
 struct RouteArgs {
