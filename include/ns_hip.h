@@ -243,7 +243,9 @@ enum {
   NS_KIND_ROUTE = 6,       /* routing with its plan, forward and backward */
   NS_KIND_EXPERTS = 7,     /* the experts' products and their gradients   */
   NS_KIND_COMBINE = 8,     /* weighted sum per token, and its gradient    */
-  NS_KIND_COUNT = 9
+  NS_KIND_RMS_NORM = 9,    /* RMS norm, forward and backward              */
+  NS_KIND_QUANTIZE = 10,   /* values to 8 bits with scales, and back      */
+  NS_KIND_COUNT = 11
 };
 int ns_timing_enable(int mask);
 int ns_timing_sample(int every, int offset);
@@ -463,6 +465,121 @@ int ns_experts_combine_backward(const void* dout, const void* y, const int32_t* 
                                 const float* weights, void* dy, float* dweights,
                                 int64_t tokens, int64_t top_k, int64_t n_rows,
                                 int64_t cols, int dtype, void* stream);
+
+/* ---- the sublayer in 8 bits ---------------------------------------------- */
+/*
+ * RMS norm with the residual's addition, values in 8 bits with scales, the
+ * experts' product of such values, and the weight gradient from rows that were
+ * kept in them.
+ *
+ * 8-bit values are e4m3 (4 exponent bits, 3 of mantissa, largest value 448, no
+ * infinity, 0x7f and 0xff are NaN).  A scale is one byte b (E8M0): 2^(b - 127).
+ *   rows      q [rows, cols], scales [rows, ceil(cols / 128)]: one for each 128
+ *             columns of a row.
+ *   weights   q [experts, fan_out, fan_in], scales [experts, ceil(fan_out / 128),
+ *             ceil(fan_in / 128)]: one for each 128 x 128 block.
+ * Last blocks may be short; cols, fan_out and fan_in are multiples of 16.  The
+ * library's scales are 2^k with the least k >= -126 for which the block's largest
+ * finite magnitude is at most 448 2^k; values are divided by it and rounded to the
+ * nearest, ties to even; infinities and NaN become NaN.  Bytes 0 to 254 are read;
+ * 255 is not a number, and so is every result that it enters.
+ *
+ * The conventions above hold.  q needs 16-byte alignment, scales none.
+ */
+
+/*
+ * ns_rms_norm - y = t rstd weight over the columns of each row, t = x + residual,
+ * rstd = 1 / sqrt(mean(t^2) + eps).
+ *
+ *   x, residual
+ *             [rows, cols] dtype, rows ldx and ldr elements apart; residual may
+ *             be NULL (t = x).
+ *   weight    [cols] param_dtype, or NULL (1).
+ *   total     [rows, cols] dtype: t, rounded; with a residual, else NULL.  The
+ *             norm is taken of t as it is stored.
+ *   y         [rows, cols] dtype, or NULL.
+ *   q, scales y as 8-bit rows (not rounded to dtype before), or both NULL.  One of
+ *             y and q is given.
+ *   rstd      fp32 [rows], or NULL; the backward pass needs it.
+ *   rows == 0 enqueues nothing.
+ */
+int ns_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                const void* weight, void* total, void* y, void* q, uint8_t* scales,
+                float* rstd, int64_t rows, int64_t cols, int dtype, int param_dtype,
+                float eps, void* stream);
+
+/*
+ * ns_rms_norm_backward - gradients of ns_rms_norm from dy [rows, cols]:
+ *   dx [rows, cols] dtype (of x and of the residual alike) and dweight [cols]
+ *   param_dtype; each may be NULL.  x is what the norm was taken of (total, where
+ *   there was a residual), weight the forward pass's (NULL: 1), rstd what it
+ *   returned.  dtotal [rows, cols] dtype, or NULL: the gradient that reaches total
+ *   from elsewhere; it is added to dx.  With rows == 0 dweight becomes zero.  Uses
+ *   library workspace (4 bytes per column and block, at most 128 MiB).
+ */
+int ns_rms_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                         const void* weight, const float* rstd, const void* dtotal,
+                         int64_t lddt, void* dx, void* dweight, int64_t rows,
+                         int64_t cols, int dtype, int param_dtype, void* stream);
+
+/* ns_quantize - x [rows, cols] dtype, rows ldx elements apart, as 8-bit rows
+ * (rows * ceil(cols / 128) below 2^32). */
+int ns_quantize(const void* x, int64_t ldx, void* q, uint8_t* scales, int64_t rows,
+                int64_t cols, int dtype, void* stream);
+
+/* ns_quantize_weights - w [experts, fan_out, fan_in] dtype as 8-bit weights, and,
+ * where qt and scales_t are not NULL, the same values transposed: qt [experts,
+ * fan_in, fan_out] with its scales.  experts <= 1024, fan_out * fan_in < 2^29. */
+int ns_quantize_weights(const void* w, void* q, uint8_t* scales, void* qt,
+                        uint8_t* scales_t, int64_t experts, int64_t fan_out,
+                        int64_t fan_in, int dtype, void* stream);
+
+/* ns_dequantize - the values x [matrices, rows, cols] dtype of q and its scales;
+ * block_rows 1: rows, 128: weights.  Exact in both types, but below 2^-126, where
+ * x is rounded. */
+int ns_dequantize(const void* q, const uint8_t* scales, void* x, int64_t matrices,
+                  int64_t rows, int64_t cols, int block_rows, int dtype, void* stream);
+
+/*
+ * ns_experts_product_scaled - ns_experts_product of 8-bit rows and weights:
+ * y[i] = x[rows[i]] W_e^T for every sorted row i of every expert e.
+ *
+ *   x, x_scales
+ *             8-bit rows [n_x, fan_in]; read through rows, x must hold less than
+ *             2 GiB.
+ *   rows      int32 [n_rows], or NULL: sorted row i is row i of x.  A row
+ *             outside [0, n_x) counts as zeros.
+ *   w, w_scales
+ *             8-bit weights [experts, fan_out, fan_in].
+ *   offsets   int32 [experts + 1], or NULL for one expert that has all rows
+ *             (a linear layer); clamped to [0, n_rows].
+ *   y         [n_rows, fan_out] dtype; rows that no expert has are not written.
+ *
+ * The gradient of x is the same product of dy in 8 bits with the transposed
+ * weights.  Results in bf16 come from the 8-bit matrix instructions, which add
+ * eight neighbouring products at a time and cut each off at 2^-13 of the largest
+ * one's power of two, everything else in fp32: at most 2^-10 of the sum of the
+ * eights' largest products, and 1.5e-5 of the result (root mean square) in rows
+ * of normal values.  Results in fp32 are fp32 sums of exact products, at half the
+ * rate.
+ */
+int ns_experts_product_scaled(const void* x, const uint8_t* x_scales, int64_t n_x,
+                              const int32_t* rows, const void* w,
+                              const uint8_t* w_scales, const int32_t* offsets, void* y,
+                              int64_t n_rows, int64_t experts, int64_t fan_out,
+                              int64_t fan_in, int dtype, void* stream);
+
+/*
+ * ns_experts_weight_grad_scaled - ns_experts_weight_grad from rows x that were
+ * kept in 8 bits: dw[e] = sum over its rows of dy[i]^T x[rows[i]], dy [n_rows,
+ * fan_out] and dw [experts, fan_out, fan_in] in dtype.  offsets is not NULL.  x is
+ * restored in dtype in library workspace (n_x rows, or n_rows without rows), which
+ * is less than 2 GiB where there are rows.
+ */
+int ns_experts_weight_grad_scaled(const void* dy, const void* x, const uint8_t* x_scales,
+                                  int64_t n_x, const int32_t* rows, const int32_t* offsets,
+                                  void* dw, int64_t n_rows, int64_t experts,
+                                  int64_t fan_out, int64_t fan_in, int dtype, void* stream);
 
 #ifdef __cplusplus
 }

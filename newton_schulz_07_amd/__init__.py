@@ -19,6 +19,7 @@ NS_DTYPE_BF16 = 1
 
 NS_KIND_SUMSQ, NS_KIND_SCALE, NS_KIND_GRAM, NS_KIND_POLY, NS_KIND_UPDATE = range(5)
 NS_KIND_LAYER_NORM, NS_KIND_ROUTE, NS_KIND_EXPERTS, NS_KIND_COMBINE = range(5, 9)
+NS_KIND_RMS_NORM, NS_KIND_QUANTIZE = range(9, 11)
 KIND_NAMES = {NS_KIND_SUMSQ: "sumsq", NS_KIND_SCALE: "scale", NS_KIND_GRAM: "gram",
               NS_KIND_POLY: "poly", NS_KIND_UPDATE: "update"}
 
@@ -59,6 +60,13 @@ SIGNATURES = {
     "ns_experts_weight_grad": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp]),
     "ns_experts_combine": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp]),
     "ns_experts_combine_backward": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp]),
+    "ns_rms_norm": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _flt, _vp]),
+    "ns_rms_norm_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _int, _int, _vp]),
+    "ns_quantize": (_int, [_vp, _i64, _vp, _vp, _i64, _i64, _int, _vp]),
+    "ns_quantize_weights": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp]),
+    "ns_dequantize": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp]),
+    "ns_experts_product_scaled": (_int, [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp]),
+    "ns_experts_weight_grad_scaled": (_int, [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp]),
 }
 
 _lib = None
@@ -342,19 +350,25 @@ def ns_stage_update(x, c_off, c_diag):
 
 # The operators' binding needs torch, which the rest of this module loads only
 # when it is called: its names are looked up on first use.
-_SUBLAYER = ("Routing", "NS_SCORE_SOFTMAX", "NS_SCORE_SIGMOID", "ns_layer_norm", "ns_layer_norm_backward", "ns_route",
-             "ns_route_backward", "ns_experts_product", "ns_experts_input_grad", "ns_experts_weight_grad",
-             "ns_experts_combine", "ns_experts_combine_backward")
+_OPERATORS = {
+    "sublayer": ("Routing", "NS_SCORE_SOFTMAX", "NS_SCORE_SIGMOID", "ns_layer_norm", "ns_layer_norm_backward",
+                 "ns_route", "ns_route_backward", "ns_experts_product", "ns_experts_input_grad",
+                 "ns_experts_weight_grad", "ns_experts_combine", "ns_experts_combine_backward"),
+    "scaled": ("Scaled", "RMSNorm", "ns_rms_norm", "ns_rms_norm_backward", "ns_quantize", "ns_quantize_weights",
+               "ns_dequantize", "ns_experts_product_scaled", "ns_experts_weight_grad_scaled"),
+}
 
 
 def __getattr__(name):
-    if name in _SUBLAYER:
-        from . import sublayer
-        for n in _SUBLAYER:
-            globals()[n] = getattr(sublayer, n)
-        return globals()[name]
+    for module, names in _OPERATORS.items():
+        if name in names:
+            from importlib import import_module
+            found = import_module(f".{module}", __name__)
+            for n in names:
+                globals()[n] = getattr(found, n)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def __dir__():
-    return sorted({*globals(), *_SUBLAYER})
+    return sorted({*globals(), *(n for names in _OPERATORS.values() for n in names)})

@@ -31,7 +31,8 @@ HIP_FLAGS = [
     "-I", CSRC,
 ]
 SOURCES = ["ns_kernels.hip", "ns_peak.hip", "ns_noalloc.hip", "ns_norm.hip", "ns_route.hip", "ns_experts.hip",
-           "ns_host.cpp", "ns_api.cpp", "ns_sublayer.cpp"]
+           "ns_rms.hip", "ns_quantize.hip", "ns_experts_scaled.hip", "ns_host.cpp", "ns_api.cpp", "ns_sublayer.cpp",
+           "ns_scaled.cpp"]
 
 
 def hipcc():
@@ -59,7 +60,7 @@ def compile_source(src, tmp, verbose=False):
 def build(verbose=False):
     tmp = os.path.join(PKG, "_build")
     os.makedirs(tmp, exist_ok=True)
-    with ThreadPoolExecutor(4) as pool:
+    with ThreadPoolExecutor(6) as pool:
         objs = list(pool.map(lambda src: compile_source(src, tmp, verbose), SOURCES))
     out_tmp = LIB + ".tmp"
     cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", out_tmp] + objs

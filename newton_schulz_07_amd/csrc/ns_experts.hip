@@ -47,83 +47,11 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "ns_device.h"
 #include "ns_lanes.h"
-#include "ns_sublayer.h"
+#include "ns_tiles.h"
 
 namespace ns {
 namespace {
-
-constexpr unsigned kOutOfRange = 0x80000000u;  // past every descriptor below
-
-struct Tile {
-  int expert, tile;  // tile: row tile within the expert
-  int begin, count;  // the expert's sorted rows
-};
-
-// Row tiles of all experts, and the running count at the end of each lane's
-// experts (lane l: experts l per .. l per + per - 1).
-__device__ __forceinline__ void expert_rows(const int* offsets, int e, int experts, int n_rows, int* begin, int* count) {
-  *begin = *count = 0;
-  if ((unsigned)e >= (unsigned)experts) return;
-  const int b = min(max(offsets[e], 0), n_rows), c = min(max(offsets[e + 1], 0), n_rows);
-  *begin = b;
-  *count = c > b ? c - b : 0;
-}
-__device__ __forceinline__ int count_tiles(const ExpertsArgs& g, int bm, int* upto) {
-  const int lane = threadIdx.x & 63, per = (g.experts + 63) / 64;
-  int n = 0;
-  for (int i = 0; i < per; ++i) {
-    int b, c;
-    expert_rows(g.offsets, lane * per + i, g.experts, g.n_rows, &b, &c);
-    n += (c + bm - 1) / bm;
-  }
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(n, o, 64);
-    if (lane >= o) n += u;
-  }
-  *upto = n;
-  return __builtin_amdgcn_readlane(n, 63);
-}
-__device__ __forceinline__ Tile find_tile(const ExpertsArgs& g, int bm, int upto, int q) {
-  const int per = (g.experts + 63) / 64;
-  const int l = __ffsll((unsigned long long)__ballot(upto > q)) - 1;
-  int left = q - (l > 0 ? __builtin_amdgcn_readlane(upto, l - 1) : 0);
-  Tile t{};
-  for (int i = 0; i < per; ++i) {
-    int b, c;
-    expert_rows(g.offsets, l * per + i, g.experts, g.n_rows, &b, &c);
-    const int n = (c + bm - 1) / bm;
-    if (left < n) {
-      t = Tile{l * per + i, left, b, c};
-      break;
-    }
-    left -= n;
-  }
-  t.expert = __builtin_amdgcn_readfirstlane(t.expert);
-  t.tile = __builtin_amdgcn_readfirstlane(t.tile);
-  t.begin = __builtin_amdgcn_readfirstlane(t.begin);
-  t.count = __builtin_amdgcn_readfirstlane(t.count);
-  return t;
-}
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ f32x4 acc_of(const f32x16& v, int rg) {  // 4 columns of a 32 x 32 block's row
-  return f32x4{v[4 * rg], v[4 * rg + 1], v[4 * rg + 2], v[4 * rg + 3]};
-}
-// bf16 pairs of 4 columns, each pair by one conversion
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ uint2 pack4(f32x4 v) {
-  return __builtin_bit_cast(uint2, __builtin_convertvector(v, bf16x4));
-}
-
-// The descriptor, in scalar registers (it is the same in every lane).
-__device__ __forceinline__ i32x4 uniform(i32x4 r) {
-  i32x4 u = {__builtin_amdgcn_readfirstlane(r[0]), __builtin_amdgcn_readfirstlane(r[1]),
-             __builtin_amdgcn_readfirstlane(r[2]), __builtin_amdgcn_readfirstlane(r[3])};
-  return u;
-}
 
 // GATHER: the weight gradient's x is read through rows.  ONCE: the weights are
 // more than the L2s hold and few rows read each (4 tokens 31 us, 38 without; with
@@ -445,42 +373,10 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   wait_vm_lgkm0<0>();  // (row numbers that nothing asked for may still be on their way)
   __syncthreads();
 
-  // 32 rows of a wave's output at a time, through its place in the LDS to whole
-  // rows of 16-byte stores.  (bf16: two lanes' four columns make one lane's
-  // eight, so the LDS is written 16 bytes at a time too.)
   T* O = reinterpret_cast<T*>(g.out) + (WG ? (size_t)tl.expert * g.fan_out * g.fan_in : (size_t)tl.begin * N);
   uint4* const mine = lds + wave * 32 * OPITCH;
 #pragma unroll
-  for (int a = 0; a < SM; ++a) {
-#pragma unroll
-    for (int b = 0; b < SN; ++b) {
-      if constexpr (ES == 2) {
-#pragma unroll
-        for (int rg = 0; rg < 4; rg += 2) {
-          const uint2 x = pack4(acc_of(acc[a][b], rg)), y = pack4(acc_of(acc[a][b], rg + 1));
-          const auto p = __builtin_amdgcn_permlane32_swap(x.x, y.x, false, false);
-          const auto q = __builtin_amdgcn_permlane32_swap(x.y, y.y, false, false);
-          mine[acc_i(lane) * OPITCH + b * 4 + rg + (lane >> 5)] = make_uint4(p[0], q[0], p[1], q[1]);
-        }
-      } else {
-#pragma unroll
-        for (int rg = 0; rg < 4; ++rg)
-          mine[acc_i(lane) * OPITCH + b * 8 + acc_j(rg, lane) / 4] =
-              __builtin_bit_cast(uint4, acc_of(acc[a][b], rg));
-      }
-    }
-    __builtin_amdgcn_wave_barrier();
-    streaming(g.stream, [&](auto stream) __attribute__((always_inline)) {
-#pragma unroll
-      for (int c0 = 0; c0 < 32 * OCH; c0 += 64) {
-        const int r = (c0 + lane) / OCH, c = (c0 + lane) % OCH;
-        const int i = i0 + wm * WTM + a * 32 + r, j = j0 + wn * WTN + c * EPC;
-        const uint4 v = mine[r * OPITCH + c];
-        if (i < m_end && j < N) store_whole<stream.value>(reinterpret_cast<uint4*>(O + (size_t)i * N + j), v);
-      }
-    });
-    __builtin_amdgcn_wave_barrier();
-  }
+  for (int a = 0; a < SM; ++a) store_32_rows<T>(acc[a], mine, O, i0 + wm * WTM + a * 32, j0 + wn * WTN, m_end, N, g.stream);
 }
 
 template <typename T, int BM, int BN, int WM, int WN, int CPR, int ST, int OCC, int MODE>

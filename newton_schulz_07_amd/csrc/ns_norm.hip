@@ -15,88 +15,11 @@
 // 1003 x 1531 fp32 (rows of odd length): 6.6, 12.6 and 4.0 us, bound by the
 // instructions of single-column accesses and by latency.
 #include "ns_device.h"
-#include "ns_lanes.h"
+#include "ns_rows.h"
 #include "ns_sublayer.h"
 
 namespace ns {
 namespace {
-
-// A thread's 8 V columns of a row, as it holds them: V vectors of 8 columns,
-// TPR vectors apart, where rows are whole vectors (kAligned: at 16-byte
-// addresses; kVectors: at any), otherwise single columns, TPR apart (kSingles:
-// a wave's access is still one run of columns).  Which columns a thread sums
-// thus goes by the row's length alone, and the result's bits do not hang on
-// how far rows are apart.  Elements past the row's end are zero, and are not
-// stored.
-enum { kAligned, kVectors, kSingles };
-template <int TPR, int HOW> __device__ __forceinline__ int column(int t, int i, int e) {
-  return HOW != kSingles ? 8 * (t + i * TPR) + e : t + TPR * (8 * i + e);
-}
-template <typename T, int TPR, int HOW>
-__device__ __forceinline__ Raw8<T> load8(const T* row, int t, int i, int cols) {
-  Raw8<T> r{};
-  if (HOW == kAligned) {
-    if (column<TPR, HOW>(t, i, 0) < cols) r = reinterpret_cast<const Raw8<T>*>(row)[t + i * TPR];
-  } else if (HOW == kVectors) {
-    if (column<TPR, HOW>(t, i, 0) < cols) __builtin_memcpy(&r, row + column<TPR, HOW>(t, i, 0), sizeof(r));
-  } else {
-    T x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = row[min(column<TPR, HOW>(t, i, e), cols - 1)];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = column<TPR, HOW>(t, i, e) < cols ? x[e] : (T)0.0f;
-    __builtin_memcpy(&r, x, sizeof(r));
-  }
-  return r;
-}
-template <typename T, int TPR, int HOW, bool STREAM>
-__device__ __forceinline__ void store8(T* row, int t, int i, int cols, const float* f) {
-  const Raw8<T> r = pack8(f, T());
-  if (HOW != kSingles) {  // (outputs are contiguous: whole vectors are aligned)
-    if (column<TPR, HOW>(t, i, 0) < cols) store_whole<STREAM>(reinterpret_cast<Raw8<T>*>(row) + t + i * TPR, r);
-  } else {
-    T x[8];
-    __builtin_memcpy(x, &r, sizeof(r));
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (column<TPR, HOW>(t, i, e) < cols) row[column<TPR, HOW>(t, i, e)] = x[e];
-  }
-}
-// the parameters of those columns (fp32 or bf16 by pdt; null: `fill`)
-template <int TPR, int V, int HOW>
-__device__ __forceinline__ void params(const void* p, int pdt, int t, int i0, int cols, float fill, float (&f)[V][8]) {
-  if (p == nullptr) {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[i][e] = fill;
-  } else if (pdt == 1) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) unpack8(load8<bf16, TPR, HOW>(reinterpret_cast<const bf16*>(p), t, i0 + i, cols), f[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) unpack8(load8<float, TPR, HOW>(reinterpret_cast<const float*>(p), t, i0 + i, cols), f[i]);
-  }
-}
-
-// Sum of (a, b) over the TPR threads of a row: one wave, or a whole block
-// (WPR waves), every thread with the same result in the same order.
-template <int WPR>
-__device__ __forceinline__ float2 row_sum(float a, float b, float2* red) {
-  a = lanes_sum<64>(a);
-  b = lanes_sum<64>(b);
-  if (WPR > 1) {
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = make_float2(a, b);
-    __syncthreads();
-    a = b = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WPR; ++w) {
-      a += red[w].x;
-      b += red[w].y;
-    }
-  }
-  return make_float2(a, b);
-}
 
 // A row takes TPR threads (a wave: four rows to a block; or the whole block)
 // of VPT vectors each.  A block walks rows with the grid's stride, so w and b
@@ -200,15 +123,9 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(const LayerNormAr
   }
 }
 
-__device__ __forceinline__ void store_param(void* p, int pdt, int c, float v) {
-  if (p == nullptr) return;
-  if (pdt == 1) reinterpret_cast<bf16*>(p)[c] = (bf16)v;
-  else reinterpret_cast<float*>(p)[c] = v;
-}
-
 // The gradients.  Each block keeps its rows' sums for dw and db in registers
 // and writes them to its own row of `partials` [blocks][2][cols], which
-// layer_norm_params_kernel adds up in a fixed order: no atomics, the same
+// norm_params_kernel adds up in a fixed order: no atomics, the same
 // bits from the same inputs.  Bound by HBM; the partial sums of 512 blocks of
 // 7168 columns are 29 MB beside the 352 MB of the rows.
 template <typename T, int TPR, int VPT, int HOW>
@@ -357,13 +274,13 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_long_kernel(const La
   }
 }
 
-// dw and db: the sum of `blocks` rows of partials, 64 columns to a block, 16
+// dw and db, or dw alone (the grid's y): the sum of `blocks` rows of partials, 64 columns to a block, 16
 // interleaved runs of rows each, joined in order.  A run's rows are on their
 // way eight at a time: latency bounds it (6 us for 29 MB, which are in the L2
 // or the last-level cache).
 constexpr int kParamRuns = 16, kParamAhead = 8;
-__global__ __launch_bounds__(64 * kParamRuns) void layer_norm_params_kernel(const float* partials, int blocks, int cols,
-                                                                            void* dw, void* db, int pdt) {
+__global__ __launch_bounds__(64 * kParamRuns) void norm_params_kernel(const float* partials, int blocks, int cols, void* dw,
+                                                                      void* db, int pdt) {
   __shared__ float sum[kParamRuns][64];
   const int lane = threadIdx.x & 63, run = threadIdx.x >> 6, c = blockIdx.x * 64 + lane, h = blockIdx.y;
   const int ld = partials_ld(cols);
@@ -373,7 +290,7 @@ __global__ __launch_bounds__(64 * kParamRuns) void layer_norm_params_kernel(cons
       float x[kParamAhead];
 #pragma unroll
       for (int u = 0; u < kParamAhead; ++u)
-        x[u] = partials[((size_t)min(p0 + u * kParamRuns, blocks - 1) * 2 + h) * ld + c];
+        x[u] = partials[((size_t)min(p0 + u * kParamRuns, blocks - 1) * gridDim.y + h) * ld + c];
 #pragma unroll
       for (int u = 0; u < kParamAhead; ++u) s += p0 + u * kParamRuns < blocks ? x[u] : 0.0f;
     }
@@ -449,8 +366,13 @@ hipError_t launch_layer_norm_backward(int dtype, const LayerNormGradArgs& args, 
     if (hipError_t e = hipGetLastError()) return e;
   }
   if (g.dw == nullptr && g.db == nullptr) return hipSuccess;
-  dispatch(layer_norm_params_kernel, dim3((unsigned)((g.cols + 63) / 64), 2), dim3(64 * kParamRuns), st,
-           (const float*)g.partials, blocks, g.cols, g.dw, g.db, g.param_dtype);
+  return launch_norm_params(g.partials, blocks, g.cols, 2, g.dw, g.db, g.param_dtype, st);
+}
+
+hipError_t launch_norm_params(const float* partials, int blocks, int cols, int sums, void* dw, void* db, int param_dtype,
+                              hipStream_t st) {
+  dispatch(norm_params_kernel, dim3((unsigned)((cols + 63) / 64), (unsigned)sums), dim3(64 * kParamRuns), st, partials,
+           blocks, cols, dw, db, param_dtype);
   return hipGetLastError();
 }
 

@@ -1,0 +1,89 @@
+// ns_scaled.h - arguments, launch rules and launch interface of RMS norm and of
+// the operators on 8-bit values with scales: quantization, the experts' product.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/ns_hip.h"
+#include "ns_layout.h"
+#include "ns_sublayer.h"
+
+namespace ns {
+
+// Columns of a row, and rows of a weight, that share a scale; blocks of n.
+constexpr int kScaleBlock = 128;
+NS_HD constexpr long long scale_blocks(long long n) { return (n + kScaleBlock - 1) / kScaleBlock; }
+
+// -------------------------------------------------------------- RMS norm
+
+struct RmsNormArgs {
+  const void *x, *residual;  // [rows, cols], rows ldx / ldr elements apart; residual null: none
+  const void* w;             // [cols] or null
+  void *total, *y;           // [rows, cols] contiguous; total with a residual, y or null
+  uint8_t *q, *scales;       // [rows, cols], [rows, blocks], or both null
+  float* rstd;               // [rows] or null
+  long long rows, ldx, ldr;
+  int cols, param_dtype;
+  float eps;
+  bool stream;  // the outputs are beyond_l2 (set at the launch, as below)
+};
+struct RmsNormGradArgs {
+  const void *dy, *x, *dtotal;  // rows lddy / ldx / lddt elements apart; dtotal null: zeros
+  const void* w;                // [cols] or null
+  const float* rstd;
+  void* dx;         // [rows, cols] contiguous, or null
+  void* dw;         // [cols] or null
+  float* partials;  // [blocks][partials_ld(cols)], null if dw is not wanted
+  long long rows, lddy, ldx, lddt;
+  int cols, param_dtype;
+  bool stream;
+};
+hipError_t launch_rms_norm(int dtype, const RmsNormArgs& g, hipStream_t st);
+// blocks: norm_backward_blocks (0 with no rows: dw becomes zero)
+hipError_t launch_rms_norm_backward(int dtype, const RmsNormGradArgs& g, int blocks, hipStream_t st);
+
+// ---------------------------------------------------------- quantization
+
+struct QuantizeArgs {
+  const void* x;  // [rows, cols], rows ldx elements apart
+  uint8_t *q, *scales;
+  long long ldx;
+  unsigned rows, cols, blocks;  // blocks: of a row
+  bool stream;
+};
+struct QuantizeWeightsArgs {
+  const void* w;                  // [experts, fan_out, fan_in]
+  uint8_t *q, *scales;            // the same, and [experts, blocks, blocks]
+  uint8_t *qt, *scales_t;         // [experts, fan_in, fan_out] and its blocks, or null
+  int experts, fan_out, fan_in;
+};
+struct DequantizeArgs {
+  const uint8_t *q, *scales;
+  void* x;
+  unsigned rows, cols, blocks;    // all matrices' rows
+  unsigned matrix_rows, matrix_blocks;  // of one matrix, and its blocks of rows (weights)
+  bool stream;
+};
+hipError_t launch_quantize(int dtype, const QuantizeArgs& g, hipStream_t st);
+hipError_t launch_quantize_weights(int dtype, const QuantizeWeightsArgs& g, hipStream_t st);
+// weights: a scale for each 128 x 128 block, not for each 128 columns of a row
+hipError_t launch_dequantize(int dtype, bool weights, const DequantizeArgs& g, hipStream_t st);
+
+// ---------------------------------------------------- the experts' product
+
+// Sorted rows as in ExpertsArgs.
+struct ScaledArgs {
+  const uint8_t *x, *x_scales;  // [n_x, fan_in], [n_x, blocks]
+  const uint8_t *w, *w_scales;  // [experts, fan_out, fan_in], [experts, blocks, blocks]
+  void* out;
+  const int* offsets;           // [experts + 1], or null: one expert has all rows
+  const int* rows;              // [n_rows], or null: row i of x
+  int n_x, n_rows, experts, fan_out, fan_in;
+  bool stream;
+};
+const char* experts_scaled_config(int dtype, const ScaledArgs& g);
+hipError_t launch_experts_scaled(int dtype, const ScaledArgs& g, hipStream_t st);
+
+}  // namespace ns

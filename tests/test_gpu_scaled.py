@@ -1,0 +1,647 @@
+"""RMS norm, 8-bit values with scales, the experts' product of them and the weight gradient from rows kept in them, on
+the GPU, against float64.
+
+Tolerances, u = 2^-24 (half a step of fp32) and h = half a step of the result's type, relative: 2^-8 for bf16, u for
+fp32; a scaled value is off by at most 2^-4 of itself, or half of the smallest step, 2^-10 scales.
+"""
+
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import newton_schulz_07_amd as ns
+from oracle import scaled as ref
+from oracle import sublayer as moe
+from tests.gpu_util import device, to64
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: U}
+DTYPES = [torch.bfloat16, torch.float32]
+# rows x cols: every way a row is held, whole vectors and single columns
+SHAPES = [(1, 8), (1, 1), (3, 16), (5, 48), (4, 512), (7, 520), (6, 1024), (5, 1040), (9, 2048), (3, 2064), (2, 4096),
+          (2, 4112), (2, 8192), (2, 8208), (2, 16384), (1, 16400), (2, 32768), (2, 32784), (1, 49168), (3, 5),
+          (5, 127), (2, 1531), (2, 2047), (1, 4097), (1, 8191), (1, 16383), (1, 32767), (1, 33001)]
+
+
+def normal(*shape, seed=0, dtype=torch.float32, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).to(device())
+
+
+def spaced(t, gap):
+    """t with its rows cols + gap elements apart."""
+    wide = torch.full((t.shape[0], t.shape[1] + gap), float("nan"), dtype=t.dtype, device=t.device)
+    wide[:, :t.shape[1]] = t
+    return wide[:, :t.shape[1]]
+
+
+def codes_of(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def same_codes(a, b):
+    """Equal codes; a NaN's sign is of no matter."""
+    return np.array_equal(a, b) or np.array_equal(ref.E4M3[a], ref.E4M3[b], equal_nan=True) and \
+        np.array_equal((a >= 128) & ~np.isnan(ref.E4M3[a]), (b >= 128) & ~np.isnan(ref.E4M3[b]))
+
+
+def check_scaled(q, s, want, slack):
+    """8-bit rows against what they stand for, known to a relative error of slack."""
+    q, s = codes_of(q), codes_of(s)
+    got = ref.values(q, s)
+    scale = np.repeat(2.0 ** (s.astype(np.float64) - 127), 128, axis=1)[:, :q.shape[1]]
+    assert np.all(np.abs(got - want) <= np.maximum(2.0 ** -4 * np.abs(want), 2.0 ** -10 * scale) * (1 + 2.0 ** -10)
+                  + slack * np.abs(want))
+    for j in range(s.shape[1]):
+        top = np.abs(want[:, j * 128:(j + 1) * 128]).max(axis=1)
+        power = 2.0 ** (s[:, j].astype(np.float64) - 127)
+        assert np.all(top <= 448 * power * (1 + slack)) and np.all((top > 224 * power * (1 - slack)) | (s[:, j] == 1))
+
+
+# -------------------------------------------------------------- RMS norm
+
+
+def norm_inputs(rows, cols, dtype, residual, gap, seed=1):
+    x = normal(rows, cols, seed=seed, dtype=dtype)
+    r = normal(rows, cols, seed=seed + 1, dtype=dtype, scale=2.0) if residual else None
+    if gap:
+        x, r = spaced(x, gap), spaced(r, 2 * gap) if residual else None
+    return x, r
+
+
+def stored_sum(x, r):
+    return x if r is None else (x.float() + r.float()).to(x.dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("residual,gap,params", [(True, 0, torch.float32), (True, 3, torch.bfloat16), (False, 8, None)])
+def test_rms_norm(dtype, rows, cols, residual, gap, params):
+    x, r = norm_inputs(rows, cols, dtype, residual, gap)
+    w = None if params is None else (1 + 0.2 * normal(cols, seed=5)).to(params)
+    eight = cols % 16 == 0
+    n = ns.ns_rms_norm(x, w, residual=r, eps=1e-5, outputs="both" if eight else "same")
+    t = stored_sum(x, r)
+    assert torch.equal(n.total, t)
+    want, rstd = ref.rms_norm(to64(t), None if w is None else to64(w), 1e-5)
+    # a thread adds at most 8 ceil(cols / 8192) squares in turn, or 32; half of that error reaches rstd
+    serial = max(32, 8 * -(-cols // 8192))
+    assert np.all(np.abs(to64(n.rstd) - rstd) <= (serial / 2 + 2) * U * rstd)
+    slack = (serial / 2 + 4) * U
+    assert np.all(np.abs(to64(n.y) - want) <= (HALF[dtype] + slack) * np.abs(want))
+    if eight:
+        check_scaled(n.q, n.scales, want, slack)
+        only = ns.ns_rms_norm(x, w, residual=r, eps=1e-5, outputs="scaled")
+        assert only.y is None
+        assert torch.equal(only.q.view(torch.uint8), n.q.view(torch.uint8))
+        assert torch.equal(only.scales.view(torch.uint8), n.scales.view(torch.uint8))
+    again = ns.ns_rms_norm(n.total, w, eps=1e-5)  # y is the norm of total as it is stored
+    assert torch.equal(again.y, n.y) and torch.equal(again.rstd, n.rstd) and again.q is None
+
+
+@pytest.mark.parametrize("rows", [1, 3, 4, 255, 2049, 9001])
+def test_rms_norm_of_many_rows(rows):
+    x, r = norm_inputs(rows, 272, torch.bfloat16, True, 0, seed=rows)
+    n = ns.ns_rms_norm(x, None, residual=r, outputs="both")
+    assert torch.equal(n.total, stored_sum(x, r))
+    want = ref.rms_norm(to64(n.total))[0]
+    assert np.all(np.abs(to64(n.y) - want) <= (HALF[torch.bfloat16] + 20 * U) * np.abs(want))
+    check_scaled(n.q, n.scales, want, 20 * U)
+
+
+def test_rms_norm_of_unusual_rows():
+    x = torch.zeros(6, 256, device=device())
+    x[1, 7] = float("nan")
+    x[2, 200] = float("inf")
+    x[3] = -0.0
+    x[4] = 1e-30
+    x[5, 130] = 1e18
+    n = ns.ns_rms_norm(x, eps=1e-6, outputs="both")
+    y = to64(n.y)
+    assert np.array_equal(y[0], np.zeros(256)) and np.array_equal(y[3], np.zeros(256))
+    assert np.isnan(y[1]).all() and np.isnan(y[2, 200]) and not y[2, :200].any()
+    assert np.allclose(y[4], 1e-27, rtol=1e-6) and abs(y[5, 130] - 16) < 1e-5
+    v = to64(ns.ns_dequantize(n.q, n.scales, dtype=torch.float32))
+    assert np.isnan(v[1]).all() and np.isnan(v[2, 200]) and not v[2, :200].any() and not v[0].any()
+    assert np.allclose(v[4], 1e-27, rtol=2.0 ** -4) and v[5, 130] == 16
+    assert codes_of(n.scales)[0].tolist() == [1, 1]
+    empty = ns.ns_rms_norm(x[:0], outputs="both")
+    assert empty.y.shape == (0, 256) and empty.scales.shape == (0, 2) and empty.rstd.shape == (0,)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("dtotal,gap,params", [(True, 0, torch.float32), (False, 3, torch.bfloat16), (True, 8, None)])
+def test_rms_norm_gradient(dtype, rows, cols, dtotal, gap, params):
+    x, dt = norm_inputs(rows, cols, dtype, dtotal, gap, seed=3)
+    dy = normal(rows, cols, seed=9, dtype=dtype)
+    w = None if params is None else (1 + 0.2 * normal(cols, seed=5)).to(params)
+    rstd = ns.ns_rms_norm(x, w).rstd
+    dx, dw = ns.ns_rms_norm_backward(dy, x, w, rstd, dtotal=dt)
+    check_gradient(dx, dw, dy, x, w, rstd, dt)
+
+
+def check_gradient(dx, dw, dy, x, w, rstd, dt):
+    dtype, (rows, cols) = x.dtype, x.shape
+    y64, t64, r64 = to64(dy), to64(x), to64(rstd)
+    w64 = None if w is None else to64(w)
+    want, want_w = ref.rms_norm_backward(y64, t64, w64, r64, None if dt is None else to64(dt))
+    g, th = y64 * (1.0 if w is None else w64), t64 * r64[:, None]
+    # the row's sum: 8 ceil(cols / 8192) or 32 products in turn, 22 joins, three roundings each
+    k = (max(32, 8 * -(-cols // 8192)) + 32) * U
+    slack = k * r64[:, None] * (np.abs(g) + np.abs(th) * np.abs(g * th).mean(axis=1, keepdims=True))
+    if dt is not None:
+        slack += 2 * U * np.abs(to64(dt))
+    assert np.all(np.abs(to64(dx) - want) <= HALF[dtype] * np.abs(want) + slack)
+    if w is None:
+        assert dw is None
+    else:  # at most all rows in turn
+        assert dw.dtype == w.dtype
+        assert np.all(np.abs(to64(dw) - want_w) <= HALF[w.dtype] * np.abs(want_w) + (rows + 8) * U * np.abs(y64 * th).sum(axis=0))
+
+
+@pytest.mark.parametrize("rows,cols", [(700, 264), (3000, 24), (1100, 4096), (5000, 77)])
+def test_rms_norm_gradient_of_many_rows(rows, cols):
+    x, dt = norm_inputs(rows, cols, torch.float32, True, 0, seed=rows)
+    dy, w = normal(rows, cols, seed=2), 1 + 0.3 * normal(cols, seed=3)
+    rstd = ns.ns_rms_norm(x, w).rstd
+    first = ns.ns_rms_norm_backward(dy, x, w, rstd, dtotal=dt)
+    check_gradient(*first, dy, x, w, rstd, dt)
+    again = ns.ns_rms_norm_backward(dy, x, w, rstd, dtotal=dt)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_rms_norm_gradient_against_differences():
+    x, w = normal(4, 80, seed=1), 1 + 0.2 * normal(80, seed=2)
+    dy, dt, d = normal(4, 80, seed=3), normal(4, 80, seed=4), to64(normal(4, 80, seed=5))
+    n = ns.ns_rms_norm(x, w, eps=1e-5)
+    dx, dw = ns.ns_rms_norm_backward(dy, x, w, n.rstd, dtotal=dt)
+
+    def loss(t, p):
+        return (to64(dy) * ref.rms_norm(t, p, 1e-5)[0]).sum() + (to64(dt) * t).sum()
+    h, x64, w64 = 1e-5, to64(x), to64(w)
+    along = (loss(x64 + h * d, w64) - loss(x64 - h * d, w64)) / (2 * h)
+    assert abs((to64(dx) * d).sum() - along) < 1e-4
+    along = (loss(x64, w64 + h * d[0]) - loss(x64, w64 - h * d[0])) / (2 * h)
+    assert abs((to64(dw) * d[0]).sum() - along) < 1e-4
+
+
+def test_rms_norm_gradient_of_no_rows():
+    x, w = torch.empty(0, 64, device=device()), torch.ones(64, device=device())
+    dx, dw = ns.ns_rms_norm_backward(x, x, w, torch.empty(0, device=device()))
+    assert dx.shape == (0, 64) and not dw.any()
+
+
+# ---------------------------------------------------------- quantization
+
+
+def unusual(rows, cols, dtype, seed=0):
+    """Values of all magnitudes, with blocks of zeros, subnormals, infinities and NaN."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g) * torch.exp(4 * torch.randn(rows, 1, generator=g))
+    kinds = torch.randint(0, 60, (rows, cols), generator=g)
+    for kind, v in enumerate((0.0, -0.0, float("inf"), float("-inf"), float("nan"), 1e-38, -2.0 ** -130, 448.0, 1.75)):
+        x[kinds == kind] = v
+    for i, v in enumerate((0.0, 2.0 ** -133, 3e38, float("nan"), 448.0, 449.0, 224.5)):
+        if i + 1 < rows:
+            x[i + 1] = v * torch.where(torch.rand(cols, generator=g) < 0.5, -1.0, 1.0)
+    return x.to(dtype).to(device())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 128), (9, 144), (33, 272), (8, 2048), (130, 112), (1, 8208), (70, 1040)])
+@pytest.mark.parametrize("gap", [0, 3, 16])
+def test_quantize(dtype, rows, cols, gap):
+    x = unusual(rows, cols, dtype, seed=rows + cols)
+    q, s = ns.ns_quantize(spaced(x, gap) if gap else x)
+    assert q.dtype == torch.float8_e4m3fn and s.dtype == torch.float8_e8m0fnu
+    want, scales = ref.quantize(to64(x))
+    assert np.array_equal(codes_of(s), scales)
+    assert same_codes(codes_of(q), want)
+
+
+def test_quantize_of_other_shapes():
+    x = unusual(30, 48, torch.float32).reshape(5, 6, 48)
+    q, s = ns.ns_quantize(x)
+    assert q.shape == (5, 6, 48) and s.shape == (5, 6, 1)
+    assert same_codes(codes_of(q).reshape(30, 48), ref.quantize(to64(x).reshape(30, 48))[0])
+    back = ns.ns_dequantize(q, s, dtype=torch.float32)
+    assert np.array_equal(to64(back).reshape(30, 48), ref.values(codes_of(q).reshape(30, 48), codes_of(s).reshape(30, 1))
+                          .astype(np.float32).astype(np.float64), equal_nan=True)
+    empty = ns.ns_quantize(x[0][:0])
+    assert empty.q.shape == (0, 48) and ns.ns_dequantize(*empty).shape == (0, 48)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("experts,fan_out,fan_in", [(1, 16, 16), (3, 128, 128), (2, 48, 272), (2, 272, 48), (1, 144, 400)])
+def test_quantize_weights(dtype, experts, fan_out, fan_in):
+    w = torch.stack([unusual(fan_out, fan_in, dtype, seed=e) for e in range(experts)])
+    (q, s), (qt, st) = ns.ns_quantize_weights(w, transposed=True)
+    alone = ns.ns_quantize_weights(w)
+    assert torch.equal(alone.q.view(torch.uint8), q.view(torch.uint8))
+    assert torch.equal(alone.scales.view(torch.uint8), s.view(torch.uint8))
+    for e in range(experts):
+        want, scales = ref.quantize(to64(w[e]), 128)
+        assert np.array_equal(codes_of(s[e]), scales) and np.array_equal(codes_of(st[e]), scales.T)
+        assert same_codes(codes_of(q[e]), want) and np.array_equal(codes_of(qt[e]), codes_of(q[e]).T)
+    for a, b in ((q, s), (qt, st)):
+        back = to64(ns.ns_dequantize(a, b, dtype=torch.float32))
+        for e in range(experts):
+            assert np.array_equal(back[e], ref.values(codes_of(a[e]), codes_of(b[e]), 128).astype(np.float32), equal_nan=True)
+    one = ns.ns_quantize_weights(w[0])
+    assert torch.equal(one.q.view(torch.uint8), q[0].view(torch.uint8)) and one.scales.shape == s.shape[1:]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_dequantize_of_every_code(dtype):
+    scales = [0, 1, 2, 60, 126, 127, 128, 200, 240, 246, 254, 255]
+    q = torch.arange(256, dtype=torch.uint8, device=device()).repeat(len(scales), 1).view(torch.float8_e4m3fn)
+    s = torch.tensor(scales, dtype=torch.uint8, device=device())[:, None].repeat(1, 2).view(torch.float8_e8m0fnu)
+    got = ns.ns_dequantize(q, s, dtype=dtype)
+    want = torch.from_numpy(ref.values(codes_of(q), codes_of(s))).to(dtype).double().numpy()
+    assert np.array_equal(to64(got), want, equal_nan=True)
+
+
+# --------------------------------------------------- the experts' product
+
+
+def routed(tokens, top_k, experts, seed, spread=1.0):
+    """(offsets, rows) of a random routing in which some experts get most."""
+    rng = np.random.default_rng(seed)
+    keys = rng.normal(size=experts) * spread + rng.normal(size=(tokens, experts))
+    flat = np.argsort(-keys, axis=1)[:, :top_k].reshape(-1)
+    order = np.argsort(flat, kind="stable")
+    offsets = np.concatenate([[0], np.cumsum(np.bincount(flat, minlength=experts))])
+    return (torch.tensor(offsets, dtype=torch.int32, device=device()),
+            torch.tensor(order // top_k, dtype=torch.int32, device=device()))
+
+
+def scaled_rows(rows, cols, seed):
+    return ns.ns_quantize(normal(rows, cols, seed=seed) * torch.exp(normal(cols, seed=seed + 1)))
+
+
+def scaled_weights(experts, fan_out, fan_in, seed):
+    return ns.ns_quantize_weights(normal(experts, fan_out, fan_in, seed=seed, scale=fan_in ** -0.5))
+
+
+def rows64(x):
+    return torch.from_numpy(ref.values(codes_of(x.q), codes_of(x.scales))).to(device())
+
+
+def weights64(w):
+    return torch.from_numpy(np.stack([ref.values(codes_of(q), codes_of(s), 128) for q, s in zip(w.q, w.scales)])).to(device())
+
+
+def check_product(y, x, w, offsets, rows, dtype):
+    """y against the sums of exact products in 64 bits."""
+    x, w = rows64(x), weights64(w)
+    y, k = y.double(), x.shape[1]
+    ends = offsets.tolist()
+    for e, (a, b) in enumerate(zip(ends, ends[1:])):
+        if a >= b:
+            continue
+        xe = x[a:b] if rows is None else x[rows[a:b].long()]
+        want = xe @ w[e].T
+        slack = 2 * k * U * (xe.abs() @ w[e].abs().T)
+        if dtype == torch.bfloat16:  # eights, each product cut at 2^-13 of the largest one's power of two
+            for k0 in range(0, k, 8):
+                top = (xe[:, None, k0:k0 + 8] * w[e][None, :, k0:k0 + 8]).abs().amax(2)
+                slack += 2.0 ** -10 * top
+        assert bool(((y[a:b] - want).abs() <= HALF[dtype] * want.abs() + slack).all()), e
+
+
+# few, some and many rows to an expert; last blocks of every length; experts without rows
+PRODUCTS = [(1, 1, 1, 16, 16), (3, 1, 2, 48, 144), (4, 2, 9, 64, 128), (5, 4, 70, 96, 272), (40, 2, 5, 144, 160),
+            (150, 3, 7, 528, 272), (300, 2, 3, 272, 1040), (700, 1, 2, 160, 2064), (65, 1, 1, 256, 128),
+            (1025, 1, 1, 272, 400), (900, 4, 6, 544, 1296), (2, 2, 200, 32, 640)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,top_k,experts,fan_out,fan_in", PRODUCTS)
+@pytest.mark.parametrize("gathered", [True, False])
+def test_product(dtype, tokens, top_k, experts, fan_out, fan_in, gathered):
+    offsets, rows = routed(tokens, top_k, experts, seed=tokens + experts)
+    n = tokens * top_k
+    x, w = scaled_rows(tokens if gathered else n, fan_in, seed=1), scaled_weights(experts, fan_out, fan_in, seed=2)
+    rows = rows if gathered else None
+    y = ns.ns_experts_product_scaled(*x, *w, offsets, rows, dtype=dtype)
+    assert y.shape == (n, fan_out) and y.dtype == dtype
+    check_product(y, x, w, offsets, rows, dtype)
+    assert torch.equal(y, ns.ns_experts_product_scaled(*x, *w, offsets, rows, dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [1, 2, 17, 33, 64, 129, 300, 1000, 2100])
+def test_product_of_one_matrix(dtype, rows):
+    x, w = scaled_rows(rows, 656, seed=rows), scaled_weights(1, 400, 656, seed=2)
+    offsets = torch.tensor([0, rows], dtype=torch.int32, device=device())
+    y = ns.ns_experts_product_scaled(*x, w.q[0], w.scales[0], dtype=dtype)
+    check_product(y, x, w, offsets, None, dtype)
+    assert torch.equal(y, ns.ns_experts_product_scaled(*x, *w, offsets, dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fan_in", [16, 112, 128, 144, 240, 256, 272, 384, 400, 512, 528, 640, 656, 784, 912, 1040, 1168, 1408])
+def test_product_of_every_count_of_stages(dtype, fan_in):
+    for rows, experts in ((20, 4), (100, 2), (600, 2)):
+        offsets = torch.tensor([0, *np.linspace(0, rows, experts + 1).astype(int)[1:]], dtype=torch.int32, device=device())
+        x, w = scaled_rows(rows, fan_in, seed=fan_in), scaled_weights(experts, 80, fan_in, seed=3)
+        check_product(ns.ns_experts_product_scaled(*x, *w, offsets, dtype=dtype), x, w, offsets, None, dtype)
+
+
+def test_product_in_fp32_is_exact_to_fp32_sums_of_widely_spread_values():
+    # eight neighbours of very different magnitudes: what the 8-bit instructions would cut off
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(64, 1024, generator=g) * torch.exp2(-torch.randint(0, 9, (64, 1024), generator=g).float())
+    w = torch.randn(1, 48, 1024, generator=g) * torch.exp2(-torch.randint(0, 9, (1, 48, 1024), generator=g).float())
+    x, w = ns.ns_quantize(x.to(device())), ns.ns_quantize_weights(w.to(device()))
+    y = ns.ns_experts_product_scaled(*x, w.q[0], w.scales[0], dtype=torch.float32).double()
+    want = rows64(x) @ weights64(w)[0].T
+    assert ((y - want).norm() / want.norm()).item() < 1024 ** 0.5 * U
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("count", [6, 40, 700])
+def test_product_leaves_out_bad_rows_and_offsets(dtype, count):
+    x, w = scaled_rows(11, 144, seed=1), scaled_weights(3, 64, 144, seed=2)
+    rows = torch.arange(count, dtype=torch.int32, device=device()) % 11
+    rows[1], rows[3], rows[5] = -1, 11, 2 ** 31 - 1
+    offsets = torch.tensor([-5, 2, 2, count - 1], dtype=torch.int32, device=device())
+    y = torch.full((count, 64), 7.0, dtype=dtype, device=device())
+    ns.ns_experts_product_scaled(*x, *w, offsets, rows, dtype=dtype, y=y)
+    assert bool((y[count - 1] == 7).all())  # behind the last sequence: left as it was
+    assert not y[[1, 3, 5][:3 if count > 6 else 2]].any()
+    good = torch.tensor([i for i in range(count - 1) if i not in (1, 3, 5)], device=device())
+    ok = rows.clamp(0, 10)
+    ends = [0, 2, 2, count - 1]
+    want = torch.empty(count - 1, 64, dtype=torch.float64, device=device())
+    for e in range(3):
+        a, b = ends[e], ends[e + 1]
+        want[a:b] = rows64(x)[ok[a:b].long()] @ weights64(w)[e].T
+    slack = (0 if dtype == torch.float32 else 2.0 ** -10) * 18 + 300 * U
+    got = y[:count - 1].double()
+    top = (rows64(x).abs().amax() * weights64(w).abs().amax()).item()
+    assert bool(((got - want)[good].abs() <= HALF[dtype] * want[good].abs() + slack * top).all())
+    for bad in ([0, 0, 0, 0], [9, 3, 1, -7], [count + 9] * 4):
+        y.fill_(7.0)
+        ns.ns_experts_product_scaled(*x, *w, torch.tensor(bad, dtype=torch.int32, device=device()), rows, dtype=dtype, y=y)
+        assert bool((y == 7).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("count", [7, 50, 400])
+def test_product_keeps_nan_in_its_row_and_column(dtype, count):
+    x = normal(count, 400, seed=1)
+    x[2, 390], x[4, 5] = float("nan"), float("inf")
+    w = normal(1, 96, 400, seed=2)
+    w[0, 50, 130] = float("inf")
+    x, w = ns.ns_quantize(x), ns.ns_quantize_weights(w)
+    x.scales.view(torch.uint8)[5, 3] = 255
+    y = ns.ns_experts_product_scaled(*x, w.q[0], w.scales[0], dtype=dtype)
+    bad = torch.zeros(count, 96, dtype=torch.bool, device=device())
+    bad[[2, 4, 5]] = True
+    bad[:, 50] = True
+    assert torch.equal(torch.isnan(y), bad)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_the_gradient_of_the_input_is_the_product_with_the_transpose(dtype):
+    offsets, rows = routed(120, 2, 4, seed=3)
+    w = normal(4, 208, 336, seed=1, scale=0.1)
+    q, qt = ns.ns_quantize_weights(w, transposed=True)
+    dy = ns.ns_quantize(normal(240, 208, seed=2))
+    dx = ns.ns_experts_product_scaled(*dy, *qt, offsets, dtype=dtype)
+    check_product(dx, dy, qt, offsets, None, dtype)
+    exact = weights64(q).transpose(1, 2)
+    assert torch.equal(weights64(qt), exact)
+
+
+# -------------------------------------------------------- weight gradient
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,top_k,experts,fan_out,fan_in", PRODUCTS)
+@pytest.mark.parametrize("gathered", [True, False])
+def test_weight_gradient(dtype, tokens, top_k, experts, fan_out, fan_in, gathered):
+    offsets, rows = routed(tokens, top_k, experts, seed=tokens + experts)
+    n = tokens * top_k
+    x, dy = scaled_rows(tokens if gathered else n, fan_in, seed=1), normal(n, fan_out, seed=2, dtype=dtype)
+    rows = rows if gathered else None
+    dw = ns.ns_experts_weight_grad_scaled(dy, *x, offsets, rows)
+    x64, ends = rows64(x), offsets.tolist()
+    for e, (a, b) in enumerate(zip(ends, ends[1:])):
+        xe = x64[a:b] if rows is None else x64[rows[a:b].long()]
+        want = dy[a:b].double().T @ xe
+        slack = 2 * (b - a) * U * (dy[a:b].double().abs().T @ xe.abs())
+        assert bool(((dw[e].double() - want).abs() <= HALF[dtype] * want.abs() + slack).all()), e
+
+
+def test_weight_gradient_of_no_rows_and_of_bad_ones():
+    x = scaled_rows(5, 32, seed=1)
+    none = torch.zeros(3, dtype=torch.int32, device=device())
+    dw = ns.ns_experts_weight_grad_scaled(torch.empty(0, 16, device=device()), x.q[:0], x.scales[:0], none)
+    assert dw.shape == (2, 16, 32) and not dw.any()
+    dy = normal(4, 16, seed=2)
+    rows = torch.tensor([0, -1, 5, 4], dtype=torch.int32, device=device())
+    offsets = torch.tensor([0, 3, 9], dtype=torch.int32, device=device())
+    dw = ns.ns_experts_weight_grad_scaled(dy, *x, offsets, rows)
+    want = torch.stack([torch.outer(dy[0].double(), rows64(x)[0]), torch.outer(dy[3].double(), rows64(x)[4])])
+    assert bool(((dw.double() - want).abs() <= 2 * U * want.abs()).all())
+
+
+# ------------------------------------------------------------ together
+
+
+class Eight:
+    """A sublayer's step in 8 bits: norm, routing, two products, combine, and the gradients of all of it."""
+
+    def __init__(self, tokens=96, width=272, hidden=144, experts=6, top_k=2, seed=0):
+        self.x = normal(tokens, width, seed=seed, dtype=torch.bfloat16)
+        self.residual = normal(tokens, width, seed=seed + 1, dtype=torch.bfloat16)
+        self.gamma = 1 + 0.1 * normal(width, seed=seed + 2)
+        self.logits = normal(tokens, experts, seed=seed + 3)
+        self.w1 = normal(experts, hidden, width, seed=seed + 4, dtype=torch.bfloat16, scale=width ** -0.5)
+        self.w2 = normal(experts, width, hidden, seed=seed + 5, dtype=torch.bfloat16, scale=hidden ** -0.5)
+        self.dout = normal(tokens, width, seed=seed + 6, dtype=torch.bfloat16)
+        self.top_k = top_k
+
+    def __call__(self):
+        w1, w1t = ns.ns_quantize_weights(self.w1, transposed=True)
+        w2, w2t = ns.ns_quantize_weights(self.w2, transposed=True)
+        r = ns.ns_route(self.logits, self.top_k)
+        n = ns.ns_rms_norm(self.x, self.gamma, residual=self.residual, outputs="scaled")
+        a = ns.ns_experts_product_scaled(n.q, n.scales, *w1, r.offsets, r.rows)
+        z = ns.ns_quantize(torch.relu(a))
+        y = ns.ns_experts_product_scaled(*z, *w2, r.offsets)
+        out = ns.ns_experts_combine(y, r.slots, r.weights)
+        dy, dp = ns.ns_experts_combine_backward(self.dout, y, r.slots, r.weights)
+        dy8 = ns.ns_quantize(dy)
+        dw2 = ns.ns_experts_weight_grad_scaled(dy, *z, r.offsets)
+        da = ns.ns_experts_product_scaled(*dy8, *w2t, r.offsets) * (a > 0)
+        dw1 = ns.ns_experts_weight_grad_scaled(da, n.q, n.scales, r.offsets, r.rows)
+        dh = ns.ns_experts_combine(ns.ns_experts_product_scaled(*ns.ns_quantize(da), *w1t, r.offsets), r.slots)
+        dx, dgamma = ns.ns_rms_norm_backward(dh, n.total, self.gamma, n.rstd, dtotal=self.dout)
+        return dict(total=n.total, rstd=n.rstd, out=out, dw1=dw1, dw2=dw2, dx=dx, dgamma=dgamma, dp=dp)
+
+
+def equal(a, b):
+    return all(torch.equal(a[k], b[k]) for k in a)
+
+
+def off(a, b):
+    return np.linalg.norm(to64(a) - b) / np.linalg.norm(b)
+
+
+def test_a_step_in_8_bits_is_near_one_in_64():
+    s = Eight()
+    got = s()
+    x, res, gamma, w1, w2, dout = (to64(t) for t in (s.x, s.residual, s.gamma, s.w1, s.w2, s.dout))
+    t = to64(got["total"])
+    h, rstd = ref.rms_norm(t, gamma)
+    ids, p, offsets, rows, slots = moe.route(to64(s.logits), s.top_k)
+    a = moe.experts_product(h, w1, offsets, rows)
+    z = np.maximum(a, 0)
+    y = moe.experts_product(z, w2, offsets)
+    out = moe.combine(y, slots, p)
+    dy, dp = moe.combine_backward(dout, y, slots, p)
+    da = moe.experts_input_grad(dy, w2, offsets) * (a > 0)
+    dh = moe.combine(moe.experts_input_grad(da, w1, offsets), slots)
+    dx, dgamma = ref.rms_norm_backward(dh, t, gamma, rstd, dout)
+    want = dict(out=out, dw1=moe.experts_weight_grad(da, h, offsets, rows), dw2=moe.experts_weight_grad(dy, z, offsets),
+                dgamma=dgamma, dx=dx, dp=dp)
+    # a rounding to e4m3 is off by 2^-4 at most, by 0.6 of that at random signs; each result has at most 8 of them
+    # behind it (weights and activations of two products, twice), whose errors add up as squares, and a relu whose
+    # sign they turn in places
+    for k, v in want.items():
+        assert off(got[k], v) < 2.0 ** -4 * 0.6 * 8 ** 0.5 * 2, (k, off(got[k], v))
+
+
+def test_a_step_gives_the_same_bits_again_and_on_another_stream():
+    s = Eight(seed=20)
+    first = s()
+    assert equal(first, s())
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        other = s()
+    stream.synchronize()
+    assert equal(first, other)
+
+
+def test_a_captured_step_replays():
+    s = Eight(seed=40)
+    first = {k: v.clone() for k, v in s().items()}
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        s()  # makes the workspaces
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            got = s()
+    torch.cuda.synchronize()
+    for i in range(3):
+        for v in got.values():
+            v.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert equal(first, got), i
+        s.x.copy_(normal(*s.x.shape, seed=50 + i, dtype=torch.bfloat16))
+        first = {k: v.clone() for k, v in s().items()}
+        torch.cuda.synchronize()
+
+
+def test_a_step_reads_no_workspace_that_it_did_not_write():
+    s = Eight(seed=60)
+    first = s()
+    ns.lib().ns_set_workspace_poison(1)
+    try:
+        assert equal(first, s())
+    finally:
+        ns.lib().ns_set_workspace_poison(0)
+
+
+def test_steps_of_two_threads():
+    steps = [Eight(seed=70), Eight(tokens=50, width=400, seed=80)]
+    want = [s() for s in steps]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i, stream):
+        with torch.cuda.stream(stream):
+            for _ in range(5):
+                got[i].append(steps[i]())
+
+    for streams in ([torch.cuda.current_stream()] * 2, [torch.cuda.Stream(), torch.cuda.Stream()]):
+        got[0].clear(), got[1].clear()
+        threads = [threading.Thread(target=work, args=(i, st)) for i, st in enumerate(streams)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert len(got[i]) == 5 and all(equal(want[i], g) for g in got[i])
+
+
+# -------------------------------------------------------------- refusals
+
+
+def test_the_binding_refuses_what_does_not_fit():
+    x, w = normal(4, 64), normal(2, 32, 64)
+    q, s = ns.ns_quantize(x)
+    wq, ws = ns.ns_quantize_weights(w)
+    o = torch.tensor([0, 2, 4], dtype=torch.int32, device=device())
+    half = x.half()
+    for error, call in [
+        (ValueError, lambda: ns.ns_rms_norm(x, residual=x[:3])),
+        (ValueError, lambda: ns.ns_rms_norm(x, residual=x.bfloat16())),
+        (ValueError, lambda: ns.ns_rms_norm(x, outputs="8")),
+        (ValueError, lambda: ns.ns_rms_norm(x, total=torch.empty_like(x))),
+        (ValueError, lambda: ns.ns_rms_norm(x, q=q)),
+        (ValueError, lambda: ns.ns_rms_norm(x, outputs="scaled", y=torch.empty_like(x))),
+        (ValueError, lambda: ns.ns_rms_norm(x, torch.ones(63, device=device()))),
+        (ValueError, lambda: ns.ns_rms_norm(x.t())),
+        (TypeError, lambda: ns.ns_rms_norm(half)),
+        (ns.NSError, lambda: ns.ns_rms_norm(x[:, :40].contiguous(), outputs="scaled")),
+        (ns.NSError, lambda: ns.ns_rms_norm(x, eps=-1.0)),
+        (ns.NSError, lambda: ns.ns_rms_norm(x, y=x)),
+        (ValueError, lambda: ns.ns_rms_norm_backward(x, x, None, torch.ones(3, device=device()))),
+        (ValueError, lambda: ns.ns_rms_norm_backward(x, x, None, torch.ones(4, device=device()), dtotal=x[:2])),
+        (ValueError, lambda: ns.ns_rms_norm_backward(x, x, None, torch.ones(4, device=device()), dweight=x[0])),
+        (TypeError, lambda: ns.ns_quantize(half)),
+        (ns.NSError, lambda: ns.ns_quantize(x[:, :40])),
+        (ValueError, lambda: ns.ns_quantize_weights(w.transpose(1, 2))),
+        (ValueError, lambda: ns.ns_quantize_weights(w[0, 0])),
+        (ns.NSError, lambda: ns.ns_quantize_weights(w[:, :24].contiguous())),
+        (TypeError, lambda: ns.ns_dequantize(x, s)),
+        (TypeError, lambda: ns.ns_dequantize(q, s.view(torch.uint8))),
+        (ValueError, lambda: ns.ns_dequantize(q, ws)),
+        (TypeError, lambda: ns.ns_dequantize(q, s, dtype=torch.float16)),
+        (TypeError, lambda: ns.ns_experts_product_scaled(x, s, wq, ws, o)),
+        (ValueError, lambda: ns.ns_experts_product_scaled(q, s[:3], wq, ws, o)),
+        (ValueError, lambda: ns.ns_experts_product_scaled(q, s, wq, ws)),
+        (ValueError, lambda: ns.ns_experts_product_scaled(q, s, wq[0], ws[0], o)),
+        (ValueError, lambda: ns.ns_experts_product_scaled(q, s, wq, ws[:, :, :0], o)),
+        (ValueError, lambda: ns.ns_experts_product_scaled(q[:, :32].contiguous(), s, wq, ws, o)),
+        (TypeError, lambda: ns.ns_experts_product_scaled(q, s, wq, ws, o, dtype=torch.float16)),
+        (TypeError, lambda: ns.ns_experts_product_scaled(q, s, wq, ws, o.long())),
+        (TypeError, lambda: ns.ns_experts_weight_grad_scaled(x[:, :32].contiguous(), x, s, o)),
+        (ValueError, lambda: ns.ns_experts_weight_grad_scaled(x[:3, :32].contiguous(), q, s, o)),
+        (ValueError, lambda: ns.ns_experts_weight_grad_scaled(x[:, :32].contiguous(), q, s, o[:1])),
+        (TypeError, lambda: ns.ns_experts_weight_grad_scaled(half[:, :32].contiguous(), q, s, o)),
+    ]:
+        with pytest.raises(error):
+            call()
+
+
+def test_what_ran_is_told():
+    x, w = scaled_rows(300, 128, seed=1), scaled_weights(1, 64, 128, seed=2)
+    ns.ns_experts_product_scaled(*x, w.q[0], w.scales[0])
+    assert "8-bit values: result=bf16 rows=300 experts=1 fan_out=64 fan_in=128" in ns.ns_query_last_config()
+    ns.ns_quantize(normal(2, 16))
+    assert ns.ns_query_last_config().startswith("quantize: dtype=fp32 rows=2 cols=16")
