@@ -35,6 +35,13 @@ __device__ __forceinline__ void dma1(unsigned lds_byte_addr, unsigned voff, i32x
                : "memory", "m0");
 }
 
+// 16 bytes per lane to a buffer; an offset out of range stores nothing.
+__device__ __forceinline__ void store16(u32x4 v, unsigned voff, i32x4 rsrc) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+      reinterpret_cast<void*>((unsigned long long)(unsigned)rsrc[0] | (unsigned long long)(unsigned)rsrc[1] << 32), 0, rsrc[2], rsrc[3]);
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)voff, 0, 0);
+}
+
 // The ring of the other products (ns_experts.hip): stage kt in slot kt % ST, its
 // loads ST - 1 stages ahead, the next step's fragments read while a step's
 // products run.  A stage is 128 bytes of k (8 chunks of 16) of BM rows of x and
@@ -72,6 +79,7 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   const int per = total / 8, rem = total % 8;
   if (local >= per + (xcd < rem ? 1 : 0)) return;
   const int lin = xcd * per + min(xcd, rem) + local;
+  int ti, tj;
   if (g.offsets != nullptr) {
     tl = find_tile(g, BM, upto, lin / tiles_n);
     if (tl.count <= 0) return;  // (only offsets that are no prefix sums lead here)
@@ -79,7 +87,9 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
     tl.tile = lin / tiles_n;
     tl.count = g.n_rows;
   }
-  const int i0 = tl.tile * BM, j0 = (lin % tiles_n) * BN;
+  // neighbours within an expert share rows of x or of w: up to 8 of its row tiles at a time, column by column
+  rect_decode(tl.tile * tiles_n + lin % tiles_n, (tl.count + BM - 1) / BM, tiles_n, ti, tj);
+  const int i0 = ti * BM, j0 = tj * BN;
 
   // Byte offsets of a wave's loads at k = 0, kOutOfRange for rows past the end.
   const bool gather = g.rows != nullptr;
@@ -260,6 +270,298 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   for (int a = 0; a < SM; ++a) store_32_rows<T>(acc[a], mine, O, i0 + wm * WTM + a * 32, j0 + wn * WTN, tl.count, N, g.stream);
 }
 
+// Large tiles: 256 x 256 by four waves, each alone on its SIMD with 128 x 128 of it,
+// one workgroup to a CU, which goes through tile after tile.
+//
+// The LDS holds two stages of 128 bytes of k.  Between a stage's 32 products (two
+// steps of 64 bytes, 16 blocks of 32 x 32 each, 64 cycles apiece) a wave issues
+// everything else:
+//   products 0 ..      the reads of the second step's fragments, two at a time
+//   product FREE       barrier: every wave has read the slot out; over the next
+//                      SPREAD products the loads of the stage two later go out
+//   product NEED       wait for the next stage's loads, barrier; the reads of its
+//                      first fragments follow
+// so that a load has 25 products' time and more to come back, which is what
+// bounds a stage: 2660 cycles at 4096 x 4096 x 14336 and 2870 in 128 experts of
+// 1536 x 2048, of which the products are 2048 (2156 without the loads).  The first
+// in us: two waves on each SIMD 267, one with a single border for both barriers 195
+// to 211, loads over 12, 16, 20 products from 10 on 186, 179, 177; lines brought to
+// the L2 ahead by loads of a byte 201.  (Half of each line a stage and four stages
+// 238: every line passes the L1 twice.)
+// The last two stages of a tile load the first two of the next one, whose place
+// and row numbers are looked up four stages ahead.  With 512 rows to each of 128
+// experts: a workgroup for each tile 256 us, this 225, where the output's stores
+// pass the L2 (nt) 241: a wave's pieces of 64 bytes then go to memory by themselves.
+// The stores are 7500 cycles of a tile's 53000.  Tiles of 256 rows are padded by a
+// quarter there.
+// v, as a value that the compiler does not know: what is computed from it for each
+// tile is not kept in registers from one tile to the next.
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+constexpr int kWide = 256, kWideFree = 9, kWideNeed = 24, kWideSpread = 22, kWideLeastStages = 4;
+
+__global__ __launch_bounds__(256, 1) void experts_scaled_wide_kernel(const ScaledArgs g) {
+  constexpr int BK = kScaleBlock, SM = 4, SN = 4, NM = SM * SN, NA = 2 * NM;
+  constexpr int LP = kWide * 8, STAGE = 2 * LP;  // chunks of 16 bytes
+  constexpr int NP = LP / 64 / 4, LD = 2 * NP + 2;  // a wave's loads of a stage: 8 of x, 8 of w, a scale of 64 rows of each
+  constexpr int READS = 2 * (SM + SN);
+  constexpr int OPITCH = 5, OUT = 32 * OPITCH;  // chunks to 32 columns of output in the LDS, and to 32 such rows
+  static_assert(2 * kWideFree >= READS && 2 * (NA - kWideNeed) >= READS, "two reads to a product");
+  static_assert(kWideFree + kWideSpread <= NA, "a stage's loads go out within one stage");
+  __shared__ uint4 ring[2 * STAGE];
+  __shared__ uint4 staging[4 * 2 * OUT];
+  __shared__ unsigned scale_ring[2 * 512];
+  __shared__ int offsets[kMaxExperts + 1];
+  __shared__ int row_numbers[256];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int N = g.fan_out, K = g.fan_in, tiles_n = (N + kWide - 1) / kWide, nk = (K + BK - 1) / BK;
+  const int kb = (int)scale_blocks(K), nb = (int)scale_blocks(N);
+  const bool gather = g.rows != nullptr;
+
+  for (int e = threadIdx.x; e <= g.experts; e += 256)
+    offsets[e] = g.offsets != nullptr ? min(max(g.offsets[e], 0), g.n_rows) : e * g.n_rows;
+  __syncthreads();
+  struct {
+    const int* offsets;
+    int experts, n_rows;
+  } const ex{offsets, g.experts, g.n_rows};
+  int upto;
+  const int row_tiles = min(count_tiles(ex, kWide, &upto), g.most_row_tiles), total = row_tiles * tiles_n;
+  // each XCD takes a contiguous run of the tiles, its workgroups one after another
+  const int xcd = blockIdx.x % 8, per = total / 8, rem = total % 8;
+  const int first_tile = xcd * per + min(xcd, rem), tiles = per + (xcd < rem ? 1 : 0);
+  int local = blockIdx.x / 8;
+  if (local >= tiles) return;
+
+  struct Place {
+    int expert, begin, count, i0, j0;
+  };
+  auto locate = [&](int at) __attribute__((always_inline)) {
+    const int lin = first_tile + at;
+    const Tile t = find_tile(ex, kWide, upto, lin / tiles_n);
+    int ti, tj;  // neighbours within an expert share rows of x or of w: up to 8 of its row tiles at a time, column by column
+    rect_decode(t.tile * tiles_n + lin % tiles_n, (max(t.count, 1) + kWide - 1) / kWide, tiles_n, ti, tj);
+    return Place{t.expert, t.begin, t.count, ti * kWide, tj * kWide};
+  };
+  // the numbers of the wave's own 64 rows of x
+  auto load_row_numbers = [&](const Place& p) __attribute__((always_inline)) {
+    const i32x4 r = uniform(make_rsrc(g.rows + p.begin + p.i0, (unsigned)max(p.count - p.i0, 0) * 4u));
+    dma4(lds_addr(reinterpret_cast<const uint4*>(row_numbers + wave * 64)), (unsigned)(wave * 64 + lane) * 4u, r);
+  };
+
+  // Where a tile's loads come from: a load covers 8 rows, lane l 16 bytes of row l / 8
+  // at the place that the ring's swizzle gives it; byte offsets at k = 0.
+  unsigned off[2 * NP], soff[2];
+  i32x4 rP, rQ, rSP, rSQ;
+  const int turn = (lane & 7) ^ (lane >> 3);
+  auto source = [&](const Place& p) __attribute__((always_inline)) {
+    const int lane = fresh(threadIdx.x & 63);
+    const int turn = (lane & 7) ^ (lane >> 3);
+    const int first = gather ? 0 : p.begin + p.i0;  // row of x at the descriptor's start
+    const int x_rows = gather ? g.n_x : max(min(min(kWide, p.count - p.i0), g.n_x - first), 0);
+    rP = uniform(make_rsrc(g.x + (size_t)first * K, (unsigned)x_rows * (unsigned)K));
+    rQ = uniform(make_rsrc(g.w + (size_t)p.expert * N * K, (unsigned)N * (unsigned)K));
+    rSP = uniform(make_rsrc(g.x_scales + (size_t)first * kb, (unsigned)x_rows * (unsigned)kb));
+    rSQ = uniform(make_rsrc(g.w_scales + (size_t)p.expert * nb * kb, (unsigned)(nb * kb)));
+    auto row_of = [&](int r) __attribute__((always_inline)) {  // r: of the wave's 64
+      const int x = gather ? row_numbers[wave * 64 + r] : wave * 64 + r;
+      return p.i0 + wave * 64 + r < p.count && (unsigned)x < (unsigned)x_rows ? x : -1;
+    };
+#pragma unroll
+    for (int t = 0; t < NP; ++t) {
+      const int x = row_of(8 * t + (lane >> 3)), j = p.j0 + wave * 64 + 8 * t + (lane >> 3);
+      const unsigned kpos = (unsigned)(turn ^ t) * 16u;
+      off[t] = x >= 0 ? (unsigned)x * (unsigned)K + kpos : kOutOfRange;
+      off[NP + t] = j < N ? (unsigned)j * (unsigned)K + kpos : kOutOfRange;
+    }
+    const int x = row_of(lane), j = p.j0 + wave * 64 + lane;
+    soff[0] = x >= 0 ? (unsigned)x * (unsigned)kb : kOutOfRange;
+    soff[1] = j < N ? (unsigned)(j / kScaleBlock) * (unsigned)kb : kOutOfRange;
+  };
+  const unsigned ring_at = lds_addr(ring), scales_at = lds_addr(reinterpret_cast<const uint4*>(scale_ring));
+  // load t of stage kt of the tile that `source` describes
+  auto issue = [&](int kt, int slot, int t, int turn16) __attribute__((always_inline)) {
+    if (t < 2 * NP) {
+      const bool in = (turn16 ^ (t % NP * 16)) < K - kt * BK;
+      const unsigned at = in ? off[t] + (unsigned)(kt * BK) : kOutOfRange;
+      const unsigned to = ring_at + (unsigned)(slot * STAGE + (t < NP ? 0 : LP) + (wave * NP + t % NP) * 64) * 16u;
+      dma16(to, at, t < NP ? rP : rQ);
+    } else {
+      const int h = t - 2 * NP;
+      dma1(scales_at + (unsigned)(slot * 512 + h * 256 + wave * 64) * 4u, soff[h] + (unsigned)kt, h ? rSQ : rSP);
+    }
+  };
+
+  f32x16 acc[SM][SN];
+#pragma unroll
+  for (int a = 0; a < SM; ++a)
+#pragma unroll
+    for (int b = 0; b < SN; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
+
+  // A step is 64 bytes of k: chunks 2 s and 2 s + 1 of each half of the wave, the
+  // same k for both operands.  The addresses move with the slot that is read.
+  int kcp[4], kcq[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    kcp[s] = kc_lane_byte(wm * 128, s, lane, 8);
+    kcq[s] = kc_lane_byte(wn * 128, s, lane, 8) + LP * 16;
+  }
+  const char* lb = reinterpret_cast<const char*>(ring);
+  struct Chunks { uint4 v[2]; };
+  Chunks pf[2][SM], qf[2][SN];
+  // read r of a step's fragments, in the order in which the products take them
+  auto read = [&](int s, int r) __attribute__((always_inline)) {
+    const int h = r & 1, o = r / 2, a = o == 0 ? 0 : o - SN, b = o - 1;
+    if (o == 0 || o > SN)
+      pf[s][a].v[h] = *reinterpret_cast<const uint4*>(lb + kcp[(2 * s + h) ^ kc_sigma(a, 8)] + a * 32 * 128);
+    else
+      qf[s][b].v[h] = *reinterpret_cast<const uint4*>(lb + kcq[(2 * s + h) ^ kc_sigma(b, 8)] + b * 32 * 128);
+  };
+  struct Scales {
+    unsigned p[SM], q[SN];
+  };
+  Scales z, z_next;
+  auto read_scales = [&](int slot, Scales& to) __attribute__((always_inline)) {
+    const unsigned* st = scale_ring + slot * 512 + (lane & 31);
+#pragma unroll
+    for (int a = 0; a < SM; ++a) to.p[a] = st[wm * 128 + 32 * a];
+#pragma unroll
+    for (int b = 0; b < SN; ++b) to.q[b] = st[256 + wn * 128 + 32 * b];
+  };
+  auto due = [](int at) { return at < kWideSpread ? at * LD / kWideSpread : LD; };  // loads out when `at` products are, from FREE on
+
+  Place here = locate(local);
+  if (gather) {
+    load_row_numbers(here);
+    wait_vm_lgkm0<0>();
+    asm volatile("" ::: "memory");
+  }
+  source(here);
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int t = 0; t < LD; ++t) issue(s, s, t, 16 * turn);
+  wait_vm_lgkm0<0>();
+  ring_barrier();
+  read_scales(0, z);
+#pragma unroll
+  for (int r = 0; r < READS; ++r) read(0, r);
+
+  // A tile's output goes out block by block (32 x 32, number j = 4 a + b): at turn t
+  // block t is rounded into one of the wave's two buffers, block t - 1 read from the
+  // other as whole rows, block t - 2 stored.  Every store is issued, rows and columns
+  // past the end out of range, so that the waits know how many are in flight.
+  constexpr int STORES = 2 * NM;
+  uint4* const mine = staging + wave * 2 * OUT;
+  u32x4 v[2][2];
+  auto turn_out = [&](int t, int lane, i32x4 rO, int j0) __attribute__((always_inline)) {
+    if (t >= 2) {
+      const int j = t - 2, col = j0 + wn * 128 + j % SN * 32 + (lane & 3) * 8;
+      const int row = wm * 128 + j / SN * 32 + (lane >> 2);
+      const unsigned at = col < N ? (unsigned)(row * N + col) * 2u : kOutOfRange;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) store16(v[j & 1][c], at + (unsigned)(c * 16 * N) * 2u, rO);
+    }
+    if (t >= 1 && t <= NM)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        v[(t - 1) & 1][c] = __builtin_bit_cast(u32x4, mine[((t - 1) & 1) * OUT + (16 * c + (lane >> 2)) * OPITCH + (lane & 3)]);
+    if (t < NM) {
+      f32x16 block = acc[t / SN][t % SN];
+      asm volatile("" : "+a"(block));  // until here it stays where the products put it
+#pragma unroll
+      for (int rg = 0; rg < 4; rg += 2) {
+        const uint2 x = pack4(acc_of(block, rg)), y = pack4(acc_of(block, rg + 1));
+        const auto p = __builtin_amdgcn_permlane32_swap(x.x, y.x, false, false);
+        const auto q = __builtin_amdgcn_permlane32_swap(x.y, y.y, false, false);
+        mine[(t & 1) * OUT + acc_i(lane) * OPITCH + rg + (lane >> 5)] = make_uint4(p[0], q[0], p[1], q[1]);
+      }
+    }
+  };
+
+  // Stage kt, in `slot`, with the loads of stage `later` of its own tile or the next.
+  // first: it is a tile's first, whose products start from zero.  The last tile's stores
+  // may be in flight too, which are newer than the loads that NEED waits for (there are
+  // none in the first tile, whose first two stages have been waited for).
+  auto stage = [&](int slot, int later, auto first) __attribute__((always_inline)) {
+    constexpr bool FIRST = decltype(first)::value;
+    const int turn16 = fresh(16 * turn);
+#pragma unroll
+    for (int n = 0; n < NA; ++n) {
+      const int s = n / NM, i = n % NM;
+      if (n == kWideFree) {
+        wait_vm_lgkm0<63>();
+        ring_barrier();
+      }
+      if (n == kWideNeed) {
+        wait_vm_lgkm0<(kWideNeed - kWideFree) * LD / kWideSpread + (FIRST ? STORES : 0)>();
+        ring_barrier();
+        read_scales(slot ^ 1, z_next);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          kcp[c] ^= STAGE * 16;
+          kcq[c] ^= STAGE * 16;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (s == 0 && 2 * i + h < READS) read(1, 2 * i + h);
+        if (n >= kWideNeed && 2 * (n - kWideNeed) + h < READS) read(0, 2 * (n - kWideNeed) + h);
+      }
+      if (n >= kWideFree)
+#pragma unroll
+        for (int t = due(n - kWideFree); t < due(n - kWideFree + 1); ++t) issue(later, slot, t, turn16);
+      __builtin_amdgcn_sched_barrier(0);  // keeps the loads and reads where they are
+      f32x16 sum = acc[i / SN][i % SN];
+      if (FIRST && s == 0) sum = f32x16{};
+      sum = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(qf[s][i % SN].v[0], qf[s][i % SN].v[1]),
+                                                            join(pf[s][i / SN].v[0], pf[s][i / SN].v[1]), sum, 0, 0, 0,
+                                                            (int)z.q[i % SN], 0, (int)z.p[i / SN]);
+      acc[i / SN][i % SN] = sum;
+    }
+    z = z_next;
+  };
+  int slot = 0;  // of the stage that is computed
+  for (;;) {
+    const bool more = local + (int)gridDim.x / 8 < tiles;
+    Place next = here;
+    auto ahead = [&](int kt) __attribute__((always_inline)) {  // what stage kt does for the next tile
+      if (kt == nk - 4 && more) {
+        next = locate(local + (int)gridDim.x / 8);
+        if (gather) load_row_numbers(next);  // (older than the loads that may be in flight at NEED)
+      }
+      if (kt == nk - 2) {
+        if (more) source(next);
+        else rP[2] = rQ[2] = rSP[2] = rSQ[2] = 0;  // nothing is left to load: all of it is out of range
+      }
+    };
+    ahead(0);
+    stage(slot, 2, std::true_type());
+    slot ^= 1;
+    for (int kt = 1; kt < nk; ++kt) {
+      ahead(kt);
+      stage(slot, kt + 2 < nk ? kt + 2 : kt + 2 - nk, std::false_type());
+      slot ^= 1;
+    }
+    const int rows = max(min(kWide, here.count - here.i0), 0), out_lane = fresh(lane);
+    const i32x4 rO = uniform(make_rsrc(reinterpret_cast<bf16*>(g.out) + (size_t)(here.begin + here.i0) * N, (unsigned)(rows * N) * 2u));
+#pragma unroll
+    for (int t = 0; t < NM + 2; ++t) turn_out(t, out_lane, rO, here.j0);
+    if (!more) break;
+    here = next;
+    local += (int)gridDim.x / 8;
+  }
+  wait_vm_lgkm0<0>();  // (loads of nothing may still be on their way to the LDS)
+}
+
 template <typename T, int BM, int BN, int WM, int WN, int ST, int OCC>
 hipError_t launch_tiles(ScaledArgs g, hipStream_t st) {
   const long long tiles_n = (g.fan_out + BN - 1) / BN;
@@ -278,28 +580,65 @@ hipError_t launch_tiles(ScaledArgs g, hipStream_t st) {
   return hipGetLastError();
 }
 
-#define NS_SCALED_WIDE 256, 256, 2, 4, 2, 1
+// Tiles of a launch: BM, BN, waves, stages, workgroups per CU.
+#define NS_SCALED_TALL 128, 256, 2, 4, 3, 1
+#define NS_SCALED_LONG 128, 128, 2, 4, 4, 1
 #define NS_SCALED_SMALL 64, 64, 2, 2, 3, 3
 #define NS_SCALED_FEW 32, 64, 1, 2, 4, 3
-enum ScaledTile { TILE_WIDE, TILE_SMALL, TILE_FEW };
+enum ScaledTile { TILE_WIDE, TILE_TALL, TILE_LONG, TILE_SMALL, TILE_FEW };
 
+// The largest tile that makes about 160 workgroups (240 of the small ones, of which
+// three share a CU): a large tile reads less for each product, a small one fills
+// the CUs and pads less.  An expert's last tile is taken as half full.  us, bf16
+// results, 1536 x 2048 if not said (N: estimated tiles):
+//   wide / tall   8 experts of 1024 rows 28 (216) / 36, of 512 rows 25 (120) / 19 (216);
+//                 128 experts of 128 rows 113 / 117, of 64 rows 107 / 99;
+//                 2048 rows, 4096 x 4096 43 (136) / 34 (264)
+//   tall / long   8 experts of 256 rows 17 (120) / 13 (240); 1024 rows, 4096 x
+//                 4096 26 (136) / 21 (272)
+//   long / small  2048 rows 11.5 (198) / 13.4, 1024 rows 10.7 (102) / 9.3; 8
+//                 experts of 128 rows 11.7 (144) / 10.8 (288)
+//   small / few   1024 rows 9.3 (396) / 10.1; 128 rows, 4096 x 4096 11.2 (160) /
+//                 8.6; 128 experts of 16 rows 80 / 73, of 32 rows 92 / 103
+// fp32 results go the same way, without the wide tile: tall / long 8 experts of 512
+// rows 29 / 36, of 256 rows 26 / 19; long / small 2048 rows 18 / 19, 1024 rows 16 / 14.
 ScaledTile choose_tile(int dtype, const ScaledArgs& g) {
   const int rows = g.n_rows / g.experts;  // an expert's, on average
-  if (rows <= 16) return TILE_FEW;
-  if (dtype == 1 && rows >= 128) return TILE_WIDE;
-  return TILE_SMALL;
+  auto tiles = [&](int bm, int bn) {
+    return ((long long)g.n_rows / bm + std::min(g.experts, g.n_rows) / 2.0) * ((g.fan_out + bn - 1) / bn);
+  };
+  if (rows > 16) {
+    if (dtype == 1 && scale_blocks(g.fan_in) >= kWideLeastStages && tiles(kWide, kWide) >= 160) return TILE_WIDE;
+    if (tiles(128, 256) >= 160) return TILE_TALL;
+    if (tiles(128, 128) >= 160) return TILE_LONG;
+    if (tiles(64, 64) >= 240) return TILE_SMALL;
+  }
+  return TILE_FEW;
+}
+
+// Row tiles of bm that n_rows rows can make: the sum of ceil(c / bm) over at most min(experts, n_rows) experts with rows.
+long long most_row_tiles(const ScaledArgs& g, int bm) {
+  return (g.n_rows + (long long)std::min(g.experts, g.n_rows) * (bm - 1)) / bm;
+}
+
+hipError_t launch_wide(ScaledArgs g, hipStream_t st) {
+  const long long most = most_row_tiles(g, kWide), tiles = most * ((g.fan_out + kWide - 1) / kWide);
+  if (tiles > 0x7fffffffll) return hipErrorInvalidValue;
+  g.most_row_tiles = (int)most;
+  const unsigned grid = (unsigned)std::min((tiles + 7) / 8 * 8, 256ll);  // a workgroup to each of the 256 CUs
+  dispatch(experts_scaled_wide_kernel, dim3(grid), dim3(256), st, g);
+  return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_type(ScaledTile tile, const ScaledArgs& g, hipStream_t st) {
   switch (tile) {
-    case TILE_WIDE:
-      if constexpr (sizeof(T) == 2) return launch_tiles<T, NS_SCALED_WIDE>(g, st);
-      break;
+    case TILE_WIDE: return sizeof(T) == 2 ? launch_wide(g, st) : hipErrorInvalidValue;
+    case TILE_TALL: return launch_tiles<T, NS_SCALED_TALL>(g, st);
+    case TILE_LONG: return launch_tiles<T, NS_SCALED_LONG>(g, st);
     case TILE_SMALL: return launch_tiles<T, NS_SCALED_SMALL>(g, st);
-    case TILE_FEW: return launch_tiles<T, NS_SCALED_FEW>(g, st);
+    default: return launch_tiles<T, NS_SCALED_FEW>(g, st);
   }
-  return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -313,6 +652,8 @@ const char* experts_scaled_config(int dtype, const ScaledArgs& g) {
 #define NS_TEXT(TILE) "experts product of 8-bit values: result=%s rows=%lld experts=%lld fan_out=%lld fan_in=%lld | tile=" TILE
   switch (choose_tile(dtype, g)) {
     case TILE_WIDE: return NS_TEXT("256x256");
+    case TILE_TALL: return NS_TEXT("128x256");
+    case TILE_LONG: return NS_TEXT("128x128");
     case TILE_SMALL: return NS_TEXT("64x64");
     default: return NS_TEXT("32x64");
   }

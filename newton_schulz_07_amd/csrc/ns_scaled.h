@@ -82,6 +82,7 @@ struct ScaledArgs {
   const int* rows;              // [n_rows], or null: row i of x
   int n_x, n_rows, experts, fan_out, fan_in;
   bool stream;
+  int most_row_tiles;  // of the tile that is launched, for offsets that ascend (set at the launch)
 };
 const char* experts_scaled_config(int dtype, const ScaledArgs& g);
 hipError_t launch_experts_scaled(int dtype, const ScaledArgs& g, hipStream_t st);

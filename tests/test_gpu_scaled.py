@@ -353,6 +353,87 @@ def test_product_of_every_count_of_stages(dtype, fan_in):
         check_product(ns.ns_experts_product_scaled(*x, *w, offsets, dtype=dtype), x, w, offsets, None, dtype)
 
 
+# shapes of the larger tiles: tokens, top_k, experts, fan_out, fan_in, tile of bf16 results, of fp32 results.  Those of
+# 256 x 256 have more tiles than CUs where fan_out is 4112, and from 4 to 10 stages
+LARGE = [(1300, 4, 9, 4112, 400, "256x256", "128x256"), (1300, 4, 9, 4112, 528, "256x256", "128x256"),
+         (1300, 4, 9, 2064, 1040, "256x256", "128x256"), (1300, 4, 9, 2064, 1168, "256x256", "128x256"),
+         (700, 2, 64, 768, 512, "128x128", "128x128"),
+         (1600, 2, 64, 1280, 512, "256x256", "128x256"), (4100, 1, 1, 2832, 656, "256x256", "128x256"),
+         (1300, 4, 9, 2064, 384, "128x256", "128x256"), (600, 4, 9, 2064, 1040, "128x256", "128x256"),
+         (600, 4, 9, 2064, 144, "128x256", "128x256"), (600, 4, 9, 2064, 400, "128x256", "128x256"),
+         (260, 4, 9, 2064, 144, "128x128", "128x128"), (260, 4, 9, 2064, 656, "128x128", "128x128"),
+         (200, 4, 9, 1040, 272, "64x64", "64x64")]
+
+
+def large_inputs(tokens, top_k, experts, fan_out, fan_in, gathered):
+    offsets, rows = routed(tokens, top_k, experts, seed=tokens, spread=0.4)
+    n = tokens * top_k
+    x, w = scaled_rows(tokens if gathered else n, fan_in, seed=1), scaled_weights(experts, fan_out, fan_in, seed=2)
+    return x, w, offsets, rows if gathered else None
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,top_k,experts,fan_out,fan_in,tile,tile32", LARGE)
+@pytest.mark.parametrize("gathered", [True, False])
+def test_product_of_large_tiles(dtype, tokens, top_k, experts, fan_out, fan_in, tile, tile32, gathered):
+    x, w, offsets, rows = large_inputs(tokens, top_k, experts, fan_out, fan_in, gathered)
+    y = ns.ns_experts_product_scaled(*x, *w, offsets, rows, dtype=dtype)
+    assert ns.ns_query_last_config().endswith("tile=" + (tile if dtype == torch.bfloat16 else tile32))
+    check_product(y, x, w, offsets, rows, dtype)
+    if experts == 1:
+        assert torch.equal(y, ns.ns_experts_product_scaled(*x, w.q[0], w.scales[0], None, rows, dtype=dtype))
+    assert torch.equal(y, ns.ns_experts_product_scaled(*x, *w, offsets, rows, dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,fan_in", [(1300, 528), (600, 400), (260, 272)])
+def test_large_tiles_keep_to_their_rows_and_columns(dtype, tokens, fan_in):
+    # rows that do not exist, experts without rows, rows behind the last expert's, NaN in a row and in a column
+    x, w, offsets, rows = large_inputs(tokens, 4, 9, 2064, fan_in, True)
+    n = rows.numel()
+    ends = offsets.clone()
+    ends[3] = ends[2]
+    ends[6:] = n - 37
+    rows = rows.clone()
+    absent = torch.tensor([0, 5, 300, n - 500, n - 38], device=device())
+    rows[absent] = torch.tensor([-1, tokens, 2 ** 31 - 1, -(2 ** 31), tokens + 7], dtype=torch.int32, device=device())
+    x.q.view(torch.uint8)[17, 131] = 0x7f
+    w.q.view(torch.uint8)[1, 1000, 77] = 0xff
+    y = torch.full((n, 2064), 7.0, dtype=dtype, device=device())
+    ns.ns_experts_product_scaled(*x, *w, ends, rows, dtype=dtype, y=y)
+    assert bool((y[n - 37:] == 7).all())
+    assert not y[absent][:, [i for i in range(2064) if i != 1000]].any()
+    bad = torch.zeros(n, 2064, dtype=torch.bool, device=device())
+    bad[rows == 17] = True
+    bad[ends[1]:ends[2], 1000] = True
+    bad[n - 37:] = False
+    assert torch.equal(torch.isnan(y), bad)
+    want = torch.empty(n - 37, 2064, dtype=torch.float64, device=device())
+    x64, w64, at = rows64(x), weights64(w), ends.tolist()
+    for e in range(9):
+        want[at[e]:at[e + 1]] = x64[rows[at[e]:at[e + 1]].clamp(0, tokens - 1).long()] @ w64[e].T
+    good = ~bad[:n - 37]
+    good[absent] = False
+    top = (x64.abs().nan_to_num().amax() * w64.abs().nan_to_num().amax()).item()  # an eight's largest product is less
+    slack = (0 if dtype == torch.float32 else 2.0 ** -10) * fan_in / 8 * top + 2 * fan_in * fan_in * U * top
+    assert bool(((y[:n - 37].double() - want)[good].abs() <= HALF[dtype] * want[good].abs() + slack).all())
+    for strange in ([0] * 10, [9, 3, 1, -7, 0, 0, 0, 0, 0, 0], [n + 9] * 10):
+        y.fill_(7.0)
+        ns.ns_experts_product_scaled(*x, *w, torch.tensor(strange, dtype=torch.int32, device=device()), rows, dtype=dtype, y=y)
+        assert bool((y == 7).all())
+
+
+def test_large_tiles_of_offsets_that_do_not_ascend():
+    # every other expert claims all rows: more tiles than rows could make; whatever is written is some expert's row
+    x, w, offsets, rows = large_inputs(1300, 4, 9, 2064, 528, False)
+    n = 5200
+    strange = torch.tensor([0, n, 0, n, 0, n, 0, n, 0, n], dtype=torch.int32, device=device())
+    guard = torch.full((n + 64, 2064), 7.0, dtype=torch.bfloat16, device=device())
+    ns.ns_experts_product_scaled(*x, *w, strange, None, y=guard[:n])
+    torch.cuda.synchronize()
+    assert bool((guard[n:] == 7).all())
+
+
 def test_product_in_fp32_is_exact_to_fp32_sums_of_widely_spread_values():
     # eight neighbours of very different magnitudes: what the 8-bit instructions would cut off
     g = torch.Generator().manual_seed(5)
