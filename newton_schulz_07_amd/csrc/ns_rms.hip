@@ -8,7 +8,7 @@
 // y is taken from t as it is stored: the backward pass and whoever else reads t
 // then see what was normalised.  dx is the gradient of x and of the residual.
 // All of it is bound by HBM; rows are held as layer norm's are (ns_rows.h,
-// norm_shape).
+// rms_shape).
 #include "ns_eight.h"
 #include "ns_rows.h"
 #include "ns_scaled.h"
@@ -274,13 +274,14 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RmsN
 
 template <typename T, int HOW, bool EIGHT>
 void launch_forward(const RmsNormArgs& g, hipStream_t st) {
-  const NormShape s = norm_shape(g.cols);
+  const NormShape s = rms_shape(g.cols);
   const dim3 grid((unsigned)norm_blocks(g.rows, s, kNormForwardBlocks)), block(s.tpr == 64 ? 256 : s.tpr);
 #define NS_RMS(TPR, VPT) \
   if (s.tpr == TPR && s.vpt == VPT) return dispatch(rms_norm_kernel<T, TPR, VPT, HOW, EIGHT>, grid, block, st, g)
   NS_RMS(64, 1);
   NS_RMS(64, 2);
   NS_RMS(64, 4);
+  if constexpr (HOW == kSingles) NS_RMS(256, 1);
   NS_RMS(256, 2);
   NS_RMS(256, 4);
   NS_RMS(1024, 2);
@@ -291,13 +292,14 @@ void launch_forward(const RmsNormArgs& g, hipStream_t st) {
 
 template <typename T, int HOW>
 void launch_backward(const RmsNormGradArgs& g, int blocks, hipStream_t st) {
-  const NormShape s = norm_shape(g.cols);
+  const NormShape s = rms_shape(g.cols);
   const dim3 grid((unsigned)blocks), block(s.tpr == 64 ? 256 : s.tpr);
 #define NS_RMS(TPR, VPT) \
   if (s.tpr == TPR && s.vpt == VPT) return dispatch(rms_norm_backward_kernel<T, TPR, VPT, HOW>, grid, block, st, g)
   NS_RMS(64, 1);
   NS_RMS(64, 2);
   NS_RMS(64, 4);
+  if constexpr (HOW == kSingles) NS_RMS(256, 1);
   NS_RMS(256, 2);
   NS_RMS(256, 4);
   NS_RMS(1024, 2);

@@ -83,7 +83,7 @@ int ns_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, c
     if (int s = check_hip(timed_launch(NS_KIND_RMS_NORM, st, [&] { return launch_rms_norm(dtype, g, st); }),
                           "rms norm launch"))
       return s;
-    const NormShape shape = norm_shape((int)cols);
+    const NormShape shape = rms_shape((int)cols);
     set_config("rms norm: dtype=%s rows=%lld cols=%lld | %lld threads x %lld vectors of 8 per row, in 8 bits: %lld",
                type_name(dtype), rows, cols, shape.tpr, shape.vpt, q != nullptr);
     return NS_OK;
@@ -120,7 +120,7 @@ int ns_rms_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ld
     if (dweight == nullptr && (rows == 0 || dx == nullptr)) return NS_OK;
     if (int s = check_arch()) return s;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const int blocks = norm_backward_blocks(rows, (int)cols);
+    const int blocks = rms_backward_blocks(rows, (int)cols);
     const size_t bytes = dweight ? (size_t)blocks * partials_ld((int)cols) * sizeof(float) : 0;
     Workspace ws;  // held to the end of the call's launches
     if (bytes > 0) {
@@ -133,7 +133,7 @@ int ns_rms_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ld
                                        [&] { return launch_rms_norm_backward(dtype, g, blocks, st); }),
                           "rms norm backward launch"))
       return s;
-    const NormShape shape = norm_shape((int)cols);
+    const NormShape shape = rms_shape((int)cols);
     set_config("rms norm backward: dtype=%s rows=%lld cols=%lld | %lld threads x %lld vectors of 8 per row, %lld blocks",
                type_name(dtype), rows, cols, shape.tpr, shape.vpt, blocks);
     return NS_OK;

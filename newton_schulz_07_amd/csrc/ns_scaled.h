@@ -40,8 +40,19 @@ struct RmsNormGradArgs {
   int cols, param_dtype;
   bool stream;
 };
+// Rows are held as layer norm's, but for those of no whole vectors and 1025 to 2048
+// columns: single columns are as many loads as there are columns to a thread, and
+// 256 threads have 8 where 64 have 32.  Forward and backward, us, fp32, 256 x 1 and
+// 64 x 4: 8192 x 2047 100 / 119, 8192 x 1531 85 / 100 (bf16 77 / 75); of 777 columns
+// 65, 64 x 2 48.
+inline NormShape rms_shape(int cols) {
+  return cols % 8 != 0 && cols > 1024 && cols <= 2048 ? NormShape{256, 1} : norm_shape(cols);
+}
+inline int rms_backward_blocks(long long rows, int cols) {
+  return (int)norm_blocks(rows, rms_shape(cols), norm_backward_blocks(1ll << 40, cols));  // as many at most
+}
 hipError_t launch_rms_norm(int dtype, const RmsNormArgs& g, hipStream_t st);
-// blocks: norm_backward_blocks (0 with no rows: dw becomes zero)
+// blocks: rms_backward_blocks (0 with no rows: dw becomes zero)
 hipError_t launch_rms_norm_backward(int dtype, const RmsNormGradArgs& g, int blocks, hipStream_t st);
 
 // ---------------------------------------------------------- quantization
