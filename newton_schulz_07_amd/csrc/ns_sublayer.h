@@ -99,9 +99,6 @@ inline int norm_backward_blocks(long long rows, int cols) {
 hipError_t launch_layer_norm(int dtype, const LayerNormArgs& g, hipStream_t st);
 // blocks: norm_backward_blocks (0 with no rows: dw and db become zero)
 hipError_t launch_layer_norm_backward(int dtype, const LayerNormGradArgs& g, int blocks, hipStream_t st);
-// dw, and db where there are two sums: those of `blocks` rows [sums][partials_ld(cols)] of partials
-hipError_t launch_norm_params(const float* partials, int blocks, int cols, int sums, void* dw, void* db, int param_dtype,
-                              hipStream_t st);
 
 // --------------------------------------------------------------- routing
 

@@ -53,6 +53,13 @@ def _row_scales(shape):
     return (*shape[:-1], _blocks(shape[-1]))
 
 
+def _eight_like(t, name, like):
+    """t, checked, or a new tensor: 8-bit values of like's shape."""
+    if t is None and like.is_contiguous():
+        return torch.empty_like(like, dtype=EIGHT)  # (takes less time than torch.empty)
+    return _out(t, name, like, EIGHT, like.shape)
+
+
 def _weight_scales(shape):
     return (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1]))
 
@@ -77,17 +84,17 @@ def ns_rms_norm(x, weight=None, residual=None, eps=1e-6, outputs="same", y=None,
         if residual.shape != x.shape or residual.dtype != x.dtype or residual.device != x.device:
             raise ValueError("residual must match x in shape, dtype and device")
         ldr = _rows_of(residual, "residual")[2]
-        total = _out(total, "total", x, x.dtype, x.shape)
+        total = _out_like(total, "total", x)
     elif total is not None:
         raise ValueError("total without a residual")
     if weight is not None:
         _dense(weight, "weight", x, None, (cols,))
     if outputs != "scaled":
-        y = _out(y, "y", x, x.dtype, x.shape)
+        y = _out_like(y, "y", x)
     elif y is not None:
         raise ValueError("y with outputs='scaled'")
     if outputs != "same":
-        q = _out(q, "q", x, EIGHT, x.shape)
+        q = _eight_like(q, "q", x)
         scales = _out(scales, "scales", x, SCALE, _row_scales(x.shape))
     elif q is not None or scales is not None:
         raise ValueError("q or scales with outputs='same'")
@@ -129,7 +136,7 @@ def ns_quantize(x, q=None, scales=None):
     """x [..., cols] fp32 or bf16 (a matrix may have spaced rows), cols a multiple of 16, as 8-bit rows: a Scaled with
     scales [..., ceil(cols / 128)]."""
     rows, cols, ld = _rows_of(x, "x")
-    q = _out(q, "q", x, EIGHT, x.shape)
+    q = _eight_like(q, "q", x)
     scales = _out(scales, "scales", x, SCALE, _row_scales(x.shape))
     _call("ns_quantize", x, x.data_ptr(), ld, q.data_ptr(), scales.data_ptr(), rows, cols, _code(x.dtype))
     return Scaled(q, scales)
@@ -167,9 +174,10 @@ def ns_dequantize(q, scales, dtype=torch.bfloat16, out=None):
     else:
         raise ValueError(f"scales of the shape {tuple(scales.shape)} belong neither to rows nor to weights of the shape "
                          f"{tuple(q.shape)}")
-    out = _out(out, "out", q, dtype, q.shape)
+    code = _code(dtype)
+    out = torch.empty_like(q, dtype=dtype) if out is None else _dense(out, "out", q, dtype, q.shape)
     _call("ns_dequantize", q, q.data_ptr(), scales.data_ptr(), out.data_ptr(), matrices, rows, cols, block_rows,
-          _code(dtype))
+          code)
     return out
 
 
