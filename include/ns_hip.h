@@ -529,14 +529,16 @@ int ns_quantize(const void* x, int64_t ldx, void* q, uint8_t* scales, int64_t ro
 
 /* ns_quantize_weights - w [experts, fan_out, fan_in] dtype as 8-bit weights, and,
  * where qt and scales_t are not NULL, the same values transposed: qt [experts,
- * fan_in, fan_out] with its scales.  experts <= 1024, fan_out * fan_in < 2^29. */
+ * fan_in, fan_out] with its scales.  experts <= 1024, fan_out * fan_in < 2^29, fewer
+ * than 2^24 blocks. */
 int ns_quantize_weights(const void* w, void* q, uint8_t* scales, void* qt,
                         uint8_t* scales_t, int64_t experts, int64_t fan_out,
                         int64_t fan_in, int dtype, void* stream);
 
 /* ns_dequantize - the values x [matrices, rows, cols] dtype of q and its scales;
  * block_rows 1: rows, 128: weights.  Exact in both types, but below 2^-126, where
- * x is rounded. */
+ * x is rounded, and past the type's largest value (scales of 2^120 and more), where
+ * it is infinite. */
 int ns_dequantize(const void* q, const uint8_t* scales, void* x, int64_t matrices,
                   int64_t rows, int64_t cols, int block_rows, int dtype, void* stream);
 
@@ -560,8 +562,10 @@ int ns_dequantize(const void* q, const uint8_t* scales, void* x, int64_t matrice
  * eight neighbouring products at a time and cut each off at 2^-13 of the largest
  * one's power of two, everything else in fp32: at most 2^-10 of the sum of the
  * eights' largest products, and 1.5e-5 of the result (root mean square) in rows
- * of normal values.  Results in fp32 are fp32 sums of exact products, at half the
- * rate.
+ * of normal values.  Results in fp32 are fp32 sums of exact products of x and w as
+ * ns_dequantize gives them in bf16, at half the rate.  A launch of 2^32 threads or
+ * more is an error: 2^30 rows and more, where it goes by tiles of 128 rows (fp32, or
+ * fan_in of at most 384).
  */
 int ns_experts_product_scaled(const void* x, const uint8_t* x_scales, int64_t n_x,
                               const int32_t* rows, const void* w,
@@ -574,7 +578,7 @@ int ns_experts_product_scaled(const void* x, const uint8_t* x_scales, int64_t n_
  * kept in 8 bits: dw[e] = sum over its rows of dy[i]^T x[rows[i]], dy [n_rows,
  * fan_out] and dw [experts, fan_out, fan_in] in dtype.  offsets is not NULL.  x is
  * restored in dtype in library workspace (n_x rows, or n_rows without rows), which
- * is less than 2 GiB where there are rows.
+ * is less than 2 GiB where there are rows, and has no such limit without.
  */
 int ns_experts_weight_grad_scaled(const void* dy, const void* x, const uint8_t* x_scales,
                                   int64_t n_x, const int32_t* rows, const int32_t* offsets,

@@ -270,6 +270,13 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   for (int a = 0; a < SM; ++a) store_32_rows<T>(acc[a], mine, O, i0 + wm * WTM + a * 32, j0 + wn * WTN, tl.count, N, g.stream);
 }
 
+// v, as a value that the compiler does not know: what is computed from it for each
+// tile is not kept in registers from one tile to the next.
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // Large tiles: 256 x 256 by four waves, each alone on its SIMD with 128 x 128 of it,
 // one workgroup to a CU, which goes through tile after tile.
 //
@@ -294,15 +301,7 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
 // pass the L2 (nt) 241: a wave's pieces of 64 bytes then go to memory by themselves.
 // The stores are 7500 cycles of a tile's 53000.  Tiles of 256 rows are padded by a
 // quarter there.
-// v, as a value that the compiler does not know: what is computed from it for each
-// tile is not kept in registers from one tile to the next.
-__device__ __forceinline__ int fresh(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-
 constexpr int kWide = 256, kWideFree = 9, kWideNeed = 24, kWideSpread = 22, kWideLeastStages = 4;
-
 __global__ __launch_bounds__(256, 1) void experts_scaled_wide_kernel(const ScaledArgs g) {
   constexpr int BK = kScaleBlock, SM = 4, SN = 4, NM = SM * SN, NA = 2 * NM;
   constexpr int LP = kWide * 8, STAGE = 2 * LP;  // chunks of 16 bytes
@@ -570,7 +569,7 @@ hipError_t launch_tiles(ScaledArgs g, hipStream_t st) {
   long long grid = ((g.n_rows + some * (BM - 1)) / BM) * tiles_n;
   grid = (grid + 7) / 8 * 8;  // every XCD reaches its last live tile
   if (grid <= 0) return hipSuccess;
-  if (grid > 0x7fffffffll) return hipErrorInvalidValue;
+  if (grid * (WM * WN * 64) >= 1ll << 32) return hipErrorInvalidValue;  // a launch holds fewer threads
   const dim3 blocks((unsigned)grid), threads(WM * WN * 64);
   constexpr bool FEW = BM == 32;
   const bool once = FEW && beyond_l2((long long)g.experts * g.fan_out * g.fan_in);

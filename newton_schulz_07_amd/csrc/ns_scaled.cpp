@@ -170,6 +170,8 @@ int ns_quantize_weights(const void* w, void* q, uint8_t* scales, void* qt, uint8
   return entry([&]() -> int {
     if (int s = check_dtype(dtype)) return s;
     if (int s = check_weights(experts, fan_out, fan_in)) return s;
+    if (block_count(experts, fan_out, fan_in) >= size_t(1) << 24)  // 256 threads each
+      return fail(NS_ERR_INVALID_ARG, "w must have fewer than 2^24 blocks");
     if (int s = check_ptr(w, "w")) return s;
     if (int s = check_ptr(q, "q")) return s;
     if (int s = check_scales(scales, "scales")) return s;

@@ -669,6 +669,77 @@ def test_steps_of_two_threads():
             assert len(got[i]) == 5 and all(equal(want[i], g) for g in got[i])
 
 
+# ----------------------------------------------------- the largest calls
+
+
+def test_rows_past_2_to_the_32_values():
+    # zeros, and 6 rows behind 2^32 values: they give what they give alone
+    rows, cols, last = (1 << 21) + 41, 2064, 6
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=device())
+    x[-last:] = normal(last, cols, seed=1, dtype=torch.bfloat16)
+    end = x[-last:].clone()
+    n, few = (ns.ns_rms_norm(t, eps=1.0, outputs="both") for t in (x, end))
+    assert torch.equal(n.y[-last:], few.y) and torch.equal(n.rstd[-last:], few.rstd) and not n.y[:-last].any()
+    assert torch.equal(n.q[-last:].view(torch.uint8), few.q.view(torch.uint8))
+    dx = ns.ns_rms_norm_backward(x, x, None, n.rstd)[0]
+    assert torch.equal(dx[-last:], ns.ns_rms_norm_backward(end, end, None, few.rstd)[0]) and not dx[:-last].any()
+    del n, dx
+    q, few = ns.ns_quantize(x), ns.ns_quantize(end)
+    for a, b in zip(q, few):
+        assert torch.equal(a[-last:].view(torch.uint8), b.view(torch.uint8))
+    ns.ns_dequantize(*q, out=x)
+    assert torch.equal(x[-last:], ns.ns_dequantize(*few)) and not x[:-last].any()
+    del x
+    w = scaled_weights(1, 48, cols, seed=2)
+    ends = torch.tensor([0, last], dtype=torch.int32, device=device())
+    for dtype in DTYPES:
+        y = ns.ns_experts_product_scaled(*q, *w, torch.tensor([0, rows], dtype=torch.int32, device=device()), dtype=dtype)
+        check_product(y[-last:], few, w, ends, None, dtype)
+        assert not y[:-last].any()
+        # and where the last rows are another expert's
+        two = ns.Scaled(*(torch.cat([t.view(torch.uint8)] * 2).view(t.dtype) for t in w))
+        offsets = torch.tensor([0, rows - last, rows], dtype=torch.int32, device=device())
+        assert torch.equal(y, ns.ns_experts_product_scaled(*q, *two, offsets, dtype=dtype))
+    dy = torch.ones(rows, 16, dtype=torch.bfloat16, device=device())
+    dw = ns.ns_experts_weight_grad_scaled(dy, *q, offsets)
+    want = rows64(few).sum(0).expand(16, cols)
+    slack = 2 * last * U * rows64(few).abs().sum(0)
+    assert not dw[0].any() and bool(((dw[1].double() - want).abs() <= HALF[torch.bfloat16] * want.abs() + slack).all())
+    del y, dy, q
+    torch.cuda.synchronize()
+    ns.lib().ns_release_workspace()
+    torch.cuda.empty_cache()
+
+
+def test_weights_past_2_to_the_32_values():
+    # experts of 2^27 values: the last one's give what they give alone, in both layouts
+    experts, fan_out, fan_in = 33, 1 << 14, 1 << 13
+    w = torch.zeros(experts, fan_out, fan_in, dtype=torch.bfloat16, device=device())
+    w[-1] = normal(fan_out, fan_in, seed=1, dtype=torch.bfloat16)
+    a, t = ns.ns_quantize_weights(w, transposed=True)
+    a1, t1 = ns.ns_quantize_weights(w[-1], transposed=True)
+    for many, one in ((a, a1), (t, t1)):
+        for m, o in zip(many, one):
+            assert torch.equal(m[-1].view(torch.uint8), o.view(torch.uint8))
+    ns.ns_dequantize(*a, out=w)
+    assert torch.equal(w[-1], ns.ns_dequantize(*a1)) and not w[:-1].any()
+    del w, t
+    x = scaled_rows(40, fan_in, seed=2)
+    offsets = torch.tensor([0] + [20] * (experts - 1) + [40], dtype=torch.int32, device=device())
+    y = ns.ns_experts_product_scaled(*x, *a, offsets)
+    assert not y[:20].any() and torch.equal(y[20:], ns.ns_experts_product_scaled(x.q[20:], x.scales[20:], *a1))
+
+
+def test_more_rows_than_a_launch_has_threads_for():
+    rows = (1 << 30) + 128
+    x, s = (torch.empty(rows, n, dtype=torch.uint8, device=device()) for n in (16, 1))
+    w = scaled_weights(1, 16, 16, seed=1)
+    with pytest.raises(ns.NSError):
+        ns.ns_experts_product_scaled(x.view(torch.float8_e4m3fn), s.view(torch.float8_e8m0fnu), *w)
+    del x, s
+    torch.cuda.empty_cache()
+
+
 # -------------------------------------------------------------- refusals
 
 

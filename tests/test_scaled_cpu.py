@@ -88,7 +88,8 @@ ALL = [("ns_rms_norm", NORM), ("ns_rms_norm_backward", NORM_BACK), ("ns_quantize
         ("ns_quantize_weights", WEIGHTS, [
             (dict(w=0), 1), (dict(q=0), 1), (dict(scales=0), 1), (dict(qt=0), 1), (dict(scales_t=0), 1),
             (dict(w=A + 8), 3), (dict(qt=D + 8), 3), (dict(fan_out=24), 3), (dict(fan_in=72), 3), (dict(experts=0), 1),
-            (dict(experts=1025), 1), (dict(fan_out=1 << 15, fan_in=1 << 14), 1), (dict(dtype=2), 2), (dict(q=A), 1),
+            (dict(experts=1025), 1), (dict(fan_out=1 << 15, fan_in=1 << 14), 1),
+            (dict(experts=1024, fan_out=1 << 14, fan_in=1 << 14), 1), (dict(dtype=2), 2), (dict(q=A), 1),
             (dict(qt=B), 1), (dict(scales_t=D + 5), 1)]),
         ("ns_dequantize", BACK, [
             (dict(q=0), 1), (dict(scales=0), 1), (dict(x=0), 1), (dict(q=A + 8), 3), (dict(x=C + 4), 3),
