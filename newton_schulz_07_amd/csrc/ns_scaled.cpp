@@ -284,7 +284,10 @@ int ns_experts_weight_grad_scaled(const void* dy, const void* x, const uint8_t* 
     if (int s = check_apart(out, in)) return s;
     if (int s = check_arch()) return s;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    // Rows that no one names are restored too: which are is known on the device only.
+    // x is restored, then it is the other weight gradient: the k of its products are rows, each with a
+    // scale of its own, which a matrix instruction on 8-bit rows could not apply.  8192 rows of 2048 take
+    // 12 of 510 us (65536 of them named, 128 experts of 1536 x 2048 bf16).  Rows that no one names are
+    // restored too: which are is known on the device only.
     const int64_t used = n_rows == 0 ? 0 : rows != nullptr ? n_x : n_rows;
     const size_t bytes = (size_t)(used * fan_in) * es;
     Workspace ws;  // held to the end of the call's launches
