@@ -24,18 +24,21 @@ __device__ __forceinline__ void expert_rows(const int* offsets, int e, int exper
   *begin = b;
   *count = c > b ? c - b : 0;
 }
+// (Offsets that ascend make fewer than 2^27.  Where experts claim the same rows again
+// and again the count stops here, so that it never turns negative.)
+constexpr int kMostTiles = (1 << 30) - 1;
 template <typename G> __device__ __forceinline__ int count_tiles(const G& g, int bm, int* upto) {
   const int lane = threadIdx.x & 63, per = (g.experts + 63) / 64;
   int n = 0;
   for (int i = 0; i < per; ++i) {
     int b, c;
     expert_rows(g.offsets, lane * per + i, g.experts, g.n_rows, &b, &c);
-    n += (c + bm - 1) / bm;
+    n = min(n + (c + bm - 1) / bm, kMostTiles);
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int u = __shfl_up(n, o, 64);
-    if (lane >= o) n += u;
+    if (lane >= o) n = min(n + u, kMostTiles);
   }
   *upto = n;
   return __builtin_amdgcn_readlane(n, 63);

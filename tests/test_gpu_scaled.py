@@ -730,6 +730,26 @@ def test_weights_past_2_to_the_32_values():
     assert not y[:20].any() and torch.equal(y[20:], ns.ns_experts_product_scaled(x.q[20:], x.scales[20:], *a1))
 
 
+def test_offsets_that_claim_more_tiles_than_32_bits_count():
+    # 512 of 1024 experts claim all of 2^29 rows: 2^31 row tiles.  Every row is one of theirs, nothing else is written.
+    rows, experts = 1 << 29, 1024
+    q, s = (torch.zeros(rows, n, dtype=torch.uint8, device=device()) for n in (16, 1))
+    q += 0x38  # 1
+    s += 127
+    w = torch.full((experts, 16, 16), 0x38, dtype=torch.uint8, device=device())
+    ws = torch.full((experts, 1, 1), 127, dtype=torch.uint8, device=device())
+    offsets = torch.tensor([0, rows] * (experts // 2) + [0], dtype=torch.int32, device=device())
+    guard = torch.full((rows + 64, 16), 7.0, dtype=torch.bfloat16, device=device())
+    ns.ns_experts_product_scaled(q.view(torch.float8_e4m3fn), s.view(torch.float8_e8m0fnu), w.view(torch.float8_e4m3fn),
+                                 ws.view(torch.float8_e8m0fnu), offsets, y=guard[:rows])
+    torch.cuda.synchronize()
+    assert bool((guard[rows:] == 7).all())
+    low, high = guard[:rows].aminmax()
+    assert low.item() >= 7 and high.item() == 16  # (a launch has tiles for rows that are claimed once)
+    del q, s, guard
+    torch.cuda.empty_cache()
+
+
 def test_more_rows_than_a_launch_has_threads_for():
     rows = (1 << 30) + 128
     x, s = (torch.empty(rows, n, dtype=torch.uint8, device=device()) for n in (16, 1))
