@@ -47,26 +47,35 @@ __device__ __forceinline__ void store16(u32x4 v, unsigned voff, i32x4 rsrc) {
 // products run.  A stage is 128 bytes of k (8 chunks of 16) of BM rows of x and
 // BN of w, and one scale byte of each row, as dwords.  x's rows are gathered on
 // the way.  T: the result's type, and with it the arithmetic.
-template <typename T, int BM, int BN, int WM, int WN, int ST, int OCC, bool ONCE>
-__global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_scaled_kernel(const ScaledArgs g) {
+// KG groups of waves share a tile, each with a ring and every KG-th block of k; the
+// first adds the others' sums to its own, in order.
+template <typename T, int BM, int BN, int WM, int WN, int ST, int OCC, int KG, bool ONCE>
+__global__ __launch_bounds__(WM* WN* KG * 64, (OCC * WM * WN * KG + 3) / 4) void experts_scaled_kernel(const ScaledArgs g) {
   constexpr bool EXACT = sizeof(T) == 4;
   constexpr int NW = WM * WN, CPR = 8, BK = 16 * CPR;
   static_assert(BK == kScaleBlock, "a stage has one scale");
   constexpr int WTM = BM / WM, WTN = BN / WN, SM = WTM / 32, SN = WTN / 32;
   constexpr int LP = BM * CPR, LQ = BN * CPR, STAGE = LP + LQ;
-  constexpr int NP = LP / 64 / NW, NQ = LQ / 64 / NW, LD = NP + NQ + 1;  // a wave's loads of a stage, one of scales
-  constexpr int SP = (BM + 63) / 64, SQ = (BN + 63) / 64;  // waves whose scale loads are x's, and w's
-  static_assert(SP + SQ <= NW, "one load of scales to a wave");
+  constexpr int SP = (BM + 63) / 64, SQ = (BN + 63) / 64;  // loads of x's scales, and of w's: one to a wave, or both to one
+  constexpr bool BOTH = NW == 1;
+  static_assert(SP + SQ <= (BOTH ? 2 : NW), "loads of scales");
+  constexpr int NP = LP / 64 / NW, NQ = LQ / 64 / NW, LD = NP + NQ + (BOTH ? 2 : 1);  // a wave's loads of a stage
+  constexpr int SCALES = (BOTH ? 2 : NW) * 64;                                         // of a stage, each a dword
   static_assert(WTM % 32 == 0 && WTN % 32 == 0, "wave tile must be whole 32x32 blocks");
   static_assert(LP % (64 * NW) == 0 && LQ % (64 * NW) == 0, "operands must split into whole wave loads");
   static_assert(ST >= 2 && ST <= 5 && LD * (ST - 2) < 64, "ring depth");
   constexpr int OPITCH = WTN / Elem<T>::kChunk + 1, OUT = NW * 32 * OPITCH;
-  __shared__ uint4 lds[ST * STAGE > OUT ? ST * STAGE : OUT];  // the ring, then the output
-  __shared__ unsigned scale_ring[ST * NW * 64];
+  constexpr int PART = SM * SN * 4 * 64;  // chunks of a wave's sums
+  static_assert(KG == 1 || OUT + (KG - 1) * NW * PART <= KG * ST * STAGE, "the groups' sums fit the ring");
+  __shared__ uint4 lds[KG * ST * STAGE > OUT ? KG * ST * STAGE : OUT];  // the rings, then the output
+  __shared__ unsigned scale_ring[KG * ST * SCALES];
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = wave_of_all % NW, group = wave_of_all / NW;
   const int wm = wave / WN, wn = wave % WN;
+  uint4* const ring = lds + group * ST * STAGE;
+  unsigned* const scales = scale_ring + group * ST * SCALES;
   const int N = g.fan_out, K = g.fan_in, tiles_n = (N + BN - 1) / BN;
   const int kb = (int)scale_blocks(K), nb = (int)scale_blocks(N);
 
@@ -116,33 +125,43 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
       off[t] = j < N ? (unsigned)j * (unsigned)K + (unsigned)d.kpos : kOutOfRange;
     }
   }
-  // The scales: wave s < SP has those of x's rows 64 s .., the next SQ those of w's.
-  unsigned soff = kOutOfRange;
-  if (wave < SP) {
-    const int r = 64 * wave + lane < BM ? row_of(64 * wave + lane) : -1;
-    if (r >= 0) soff = (unsigned)r * (unsigned)kb;
-  } else if (wave < SP + SQ) {
-    const int j = j0 + 64 * (wave - SP) + lane;
-    if (64 * (wave - SP) + lane < BN && j < N) soff = (unsigned)(j / kScaleBlock) * (unsigned)kb;
+  // The scales: load s < SP has those of x's rows 64 s .., the next SQ those of w's.
+  unsigned soff[BOTH ? 2 : 1];
+  i32x4 rS[BOTH ? 2 : 1];
+#pragma unroll
+  for (int u = 0; u < (BOTH ? 2 : 1); ++u) {
+    const int s = BOTH ? u : wave;
+    soff[u] = kOutOfRange;
+    if (s < SP) {
+      const int r = 64 * s + lane < BM ? row_of(64 * s + lane) : -1;
+      if (r >= 0) soff[u] = (unsigned)r * (unsigned)kb;
+    } else if (s < SP + SQ) {
+      const int j = j0 + 64 * (s - SP) + lane;
+      if (64 * (s - SP) + lane < BN && j < N) soff[u] = (unsigned)(j / kScaleBlock) * (unsigned)kb;
+    }
+    rS[u] = uniform(s < SP ? make_rsrc(g.x_scales + (size_t)first * kb, (unsigned)x_rows * (unsigned)kb)
+                           : make_rsrc(g.w_scales + (size_t)tl.expert * nb * kb, (unsigned)(nb * kb)));
   }
-  const i32x4 rS = uniform(wave < SP ? make_rsrc(g.x_scales + (size_t)first * kb, (unsigned)x_rows * (unsigned)kb)
-                                     : make_rsrc(g.w_scales + (size_t)tl.expert * nb * kb, (unsigned)(nb * kb)));
 
   auto issue = [&](int kt, int slot, auto whole) __attribute__((always_inline)) {
     constexpr bool WHOLE = decltype(whole)::value;
-    const int k0 = kt * BK;
+    const int block = kt * KG + group, k0 = block * BK;
     const bool all = WHOLE || k0 + BK <= K;
 #pragma unroll
     for (int t = 0; t < NP + NQ; ++t) {
       const int idx = t < NP ? wave * NP + t : LP / 64 + wave * NQ + t - NP;
       const unsigned at = all || k0 + dma_src(idx, lane, BM, BN, CPR, 16, false, false, 1).kpos < K ? off[t] + (unsigned)k0
                                                                                                     : kOutOfRange;
-      const unsigned to = lds_addr(lds + slot * STAGE + idx * 64);
+      const unsigned to = lds_addr(ring + slot * STAGE + idx * 64);
       if (t < NP) dma16(to, at, rP);
       else if constexpr (ONCE) dma16_once(to, at, rQ);
       else dma16(to, at, rQ);
     }
-    dma1(lds_addr(reinterpret_cast<const uint4*>(scale_ring + (slot * NW + wave) * 64)), soff + (unsigned)kt, rS);
+#pragma unroll
+    for (int u = 0; u < (BOTH ? 2 : 1); ++u) {  // (past the row's last block there is no scale of its own)
+      const unsigned at = KG == 1 || WHOLE || block < kb ? soff[u] + (unsigned)block : kOutOfRange;
+      dma1(lds_addr(reinterpret_cast<const uint4*>(scales + slot * SCALES + (BOTH ? u : wave) * 64)), at, rS[u]);
+    }
   };
 
   f32x16 acc[SM][SN];
@@ -162,7 +181,7 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
     kcp[s] = kc_lane_byte(wm * WTM, s, lane, CPR);
     kcq[s] = kc_lane_byte(wn * WTN, s, lane, CPR) + LP * 16;
   }
-  const char* lb = reinterpret_cast<const char*>(lds);
+  const char* lb = reinterpret_cast<const char*>(ring);
   struct Chunks { uint4 v[2]; };
   auto load_step = [&](int slot, int s, Chunks (&pf)[SM], Chunks (&qf)[SN]) __attribute__((always_inline)) {
     const char* st = lb + slot * STAGE * 16;
@@ -177,14 +196,14 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
     }
   };
   auto load_scales = [&](int slot, unsigned (&sp)[SM], unsigned (&sq)[SN]) __attribute__((always_inline)) {
-    const unsigned* st = scale_ring + slot * NW * 64 + (lane & 31);
+    const unsigned* st = scales + slot * SCALES + (lane & 31);
 #pragma unroll
     for (int a = 0; a < SM; ++a) sp[a] = st[wm * WTM + 32 * a];
 #pragma unroll
     for (int b = 0; b < SN; ++b) sq[b] = st[SP * 64 + wn * WTN + 32 * b];
   };
 
-  const int nk = (K + BK - 1) / BK;
+  const int nk = (kb + KG - 1) / KG;
   Chunks pf[2][SM], qf[2][SN];
   unsigned sp[2][SM], sq[2][SN];
   auto wait_stage = [&](int kt, auto steady) __attribute__((always_inline)) {
@@ -263,6 +282,33 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
   for (int u = 0; u < UN + ST - 1; ++u)
     if (kt0 + u < nk) stage(kt0 + u, u, std::false_type());
   __syncthreads();
+  if constexpr (KG > 1) {
+    float4* const part = reinterpret_cast<float4*>(lds + OUT) + wave * PART + lane;
+    auto place = [&](int from, int a, int b, int rg) { return part + (from - 1) * NW * PART + ((a * SN + b) * 4 + rg) * 64; };
+#pragma unroll
+    for (int a = 0; a < SM; ++a)
+#pragma unroll
+      for (int b = 0; b < SN; ++b)
+#pragma unroll
+        for (int rg = 0; rg < 4; ++rg)
+          if (group > 0) *place(group, a, b, rg) = __builtin_bit_cast(float4, acc_of(acc[a][b], rg));
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int from = 1; from < KG; ++from)
+#pragma unroll
+      for (int a = 0; a < SM; ++a)
+#pragma unroll
+        for (int b = 0; b < SN; ++b)
+#pragma unroll
+          for (int rg = 0; rg < 4; ++rg) {
+            const float4 v = *place(from, a, b, rg);
+            acc[a][b][4 * rg] += v.x;
+            acc[a][b][4 * rg + 1] += v.y;
+            acc[a][b][4 * rg + 2] += v.z;
+            acc[a][b][4 * rg + 3] += v.w;
+          }
+  }
 
   T* O = reinterpret_cast<T*>(g.out) + (size_t)tl.begin * N;
   uint4* const mine = lds + wave * 32 * OPITCH;
@@ -561,7 +607,7 @@ __global__ __launch_bounds__(256, 1) void experts_scaled_wide_kernel(const Scale
   wait_vm_lgkm0<0>();  // (loads of nothing may still be on their way to the LDS)
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int ST, int OCC>
+template <typename T, int BM, int BN, int WM, int WN, int ST, int OCC, int KG>
 hipError_t launch_tiles(ScaledArgs g, hipStream_t st) {
   const long long tiles_n = (g.fan_out + BN - 1) / BN;
   // sum of ceil(c / BM) over at most min(experts, n_rows) non-empty experts
@@ -569,22 +615,28 @@ hipError_t launch_tiles(ScaledArgs g, hipStream_t st) {
   long long grid = ((g.n_rows + some * (BM - 1)) / BM) * tiles_n;
   grid = (grid + 7) / 8 * 8;  // every XCD reaches its last live tile
   if (grid <= 0) return hipSuccess;
-  if (grid * (WM * WN * 64) >= 1ll << 32) return hipErrorInvalidValue;  // a launch holds fewer threads
-  const dim3 blocks((unsigned)grid), threads(WM * WN * 64);
+  if (grid * (WM * WN * KG * 64) >= 1ll << 32) return hipErrorInvalidValue;  // a launch holds fewer threads
+  const dim3 blocks((unsigned)grid), threads(WM * WN * KG * 64);
   constexpr bool FEW = BM == 32;
   const bool once = FEW && beyond_l2((long long)g.experts * g.fan_out * g.fan_in);
   g.stream = beyond_l2((long long)g.n_rows * g.fan_out * (long long)sizeof(T));
-  if (once) dispatch(experts_scaled_kernel<T, BM, BN, WM, WN, ST, OCC, FEW>, blocks, threads, st, g);
-  else dispatch(experts_scaled_kernel<T, BM, BN, WM, WN, ST, OCC, false>, blocks, threads, st, g);
+  if (once) dispatch(experts_scaled_kernel<T, BM, BN, WM, WN, ST, OCC, KG, FEW>, blocks, threads, st, g);
+  else dispatch(experts_scaled_kernel<T, BM, BN, WM, WN, ST, OCC, KG, false>, blocks, threads, st, g);
   return hipGetLastError();
 }
 
-// Tiles of a launch: BM, BN, waves, stages, workgroups per CU.
-#define NS_SCALED_TALL 128, 256, 2, 4, 3, 1
-#define NS_SCALED_LONG 128, 128, 2, 4, 4, 1
-#define NS_SCALED_SMALL 64, 64, 2, 2, 3, 3
-#define NS_SCALED_FEW 32, 64, 1, 2, 4, 3
-enum ScaledTile { TILE_WIDE, TILE_TALL, TILE_LONG, TILE_SMALL, TILE_FEW };
+// Tiles of a launch: BM, BN, waves, stages, workgroups per CU, groups of waves.
+#define NS_SCALED_TALL 128, 256, 2, 4, 3, 1, 1
+#define NS_SCALED_LONG 128, 128, 2, 4, 4, 1, 1
+#define NS_SCALED_SMALL 64, 64, 2, 2, 3, 3, 1
+#define NS_SCALED_FEW 32, 64, 1, 2, 4, 3, 1
+#define NS_SCALED_SPLIT 32, 32, 1, 1, 4, 1, 4
+enum ScaledTile { TILE_WIDE, TILE_TALL, TILE_LONG, TILE_SMALL, TILE_FEW, TILE_SPLIT };
+
+// Row tiles of bm that n_rows rows can make: the sum of ceil(c / bm) over at most min(experts, n_rows) experts with rows.
+long long most_row_tiles(const ScaledArgs& g, int bm) {
+  return (g.n_rows + (long long)std::min(g.experts, g.n_rows) * (bm - 1)) / bm;
+}
 
 // The largest tile that makes about 160 workgroups (240 of the small ones, of which
 // three share a CU): a large tile reads less for each product, a small one fills
@@ -601,6 +653,20 @@ enum ScaledTile { TILE_WIDE, TILE_TALL, TILE_LONG, TILE_SMALL, TILE_FEW };
 //                 8.6; 128 experts of 16 rows 80 / 73, of 32 rows 92 / 103
 // fp32 results go the same way, without the wide tile: tall / long 8 experts of 512
 // rows 29 / 36, of 256 rows 26 / 19; long / small 2048 rows 18 / 19, 1024 rows 16 / 14.
+//
+// Where tiles of 32 x 32 leave no CU more than one, and so few workgroups would wait
+// for their loads one after another, four groups of waves share k (split), each with
+// three stages on their way.  32 x 64 / split, us, one matrix, in a graph if below 8:
+//   1 row: 4096 x 14336 29 / 15 (58.7 MB: 11.3 at a large copy's rate), 16 rows of
+//   4096 x 4096 8.1 / 6.2, 1536 x 2048 5.1 / 4.4, x 512 3.7 / 3.4, x 384 3.5 / 3.4, x 256
+//   3.3 / 3.4, x 128 3.1 / 3.4; 64 rows of 4096 x 14336 32 / 21, 128 rows of 2048 x 7168
+//   (256 tiles) 11.5 / 8.7; 4 of 16 experts of 2048 x 7168 (256) 17.5 / 11.8; with more
+//   tiles 1 row of 14336 x 4096 (448) 12.2 / 13.8, 128 rows of 4096 x 14336 (512) 32 / 39,
+//   32 experts of 1536 x 2048 16 / 27.  fp32 results: 4096 x 14336 35 / 17, 16 rows of
+//   4096 x 4096 12.3 / 7.7, 1536 x 384 3.9 / 3.6, x 256 3.5 / 3.6.
+// (Two groups, two workgroups to a CU: 17 in the first case and 4 % less at 1536 x 512;
+// 32 x 64 by four groups 23; six or eight groups with fewer stages 16 and 22.)
+constexpr int kCUs = 256, kSplitLeastBlocks = 4;
 ScaledTile choose_tile(int dtype, const ScaledArgs& g) {
   const int rows = g.n_rows / g.experts;  // an expert's, on average
   auto tiles = [&](int bm, int bn) {
@@ -612,19 +678,15 @@ ScaledTile choose_tile(int dtype, const ScaledArgs& g) {
     if (tiles(128, 128) >= 160) return TILE_LONG;
     if (tiles(64, 64) >= 240) return TILE_SMALL;
   }
+  if (most_row_tiles(g, 32) * ((g.fan_out + 31) / 32) <= kCUs && scale_blocks(g.fan_in) >= kSplitLeastBlocks) return TILE_SPLIT;
   return TILE_FEW;
-}
-
-// Row tiles of bm that n_rows rows can make: the sum of ceil(c / bm) over at most min(experts, n_rows) experts with rows.
-long long most_row_tiles(const ScaledArgs& g, int bm) {
-  return (g.n_rows + (long long)std::min(g.experts, g.n_rows) * (bm - 1)) / bm;
 }
 
 hipError_t launch_wide(ScaledArgs g, hipStream_t st) {
   const long long most = most_row_tiles(g, kWide), tiles = most * ((g.fan_out + kWide - 1) / kWide);
   if (tiles > 0x7fffffffll) return hipErrorInvalidValue;
   g.most_row_tiles = (int)most;
-  const unsigned grid = (unsigned)std::min((tiles + 7) / 8 * 8, 256ll);  // a workgroup to each of the 256 CUs
+  const unsigned grid = (unsigned)std::min((tiles + 7) / 8 * 8, (long long)kCUs);  // a workgroup to each CU
   dispatch(experts_scaled_wide_kernel, dim3(grid), dim3(256), st, g);
   return hipGetLastError();
 }
@@ -636,6 +698,7 @@ hipError_t launch_type(ScaledTile tile, const ScaledArgs& g, hipStream_t st) {
     case TILE_TALL: return launch_tiles<T, NS_SCALED_TALL>(g, st);
     case TILE_LONG: return launch_tiles<T, NS_SCALED_LONG>(g, st);
     case TILE_SMALL: return launch_tiles<T, NS_SCALED_SMALL>(g, st);
+    case TILE_SPLIT: return launch_tiles<T, NS_SCALED_SPLIT>(g, st);
     default: return launch_tiles<T, NS_SCALED_FEW>(g, st);
   }
 }
@@ -654,6 +717,7 @@ const char* experts_scaled_config(int dtype, const ScaledArgs& g) {
     case TILE_TALL: return NS_TEXT("128x256");
     case TILE_LONG: return NS_TEXT("128x128");
     case TILE_SMALL: return NS_TEXT("64x64");
+    case TILE_SPLIT: return NS_TEXT("32x32, k by 4 groups of waves");
     default: return NS_TEXT("32x64");
   }
 #undef NS_TEXT

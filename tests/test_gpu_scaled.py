@@ -365,6 +365,34 @@ LARGE = [(1300, 4, 9, 4112, 400, "256x256", "128x256"), (1300, 4, 9, 4112, 528, 
          (200, 4, 9, 1040, 272, "64x64", "64x64")]
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fan_in", [512, 528, 640, 784, 896, 1024, 1040, 1424, 1552, 2048, 2064, 4624])
+def test_product_of_few_tiles_by_groups_of_waves(dtype, fan_in):
+    # every number of blocks that the last round leaves to the groups, the last one short or not
+    for tokens, experts, fan_out in ((1, 1, 48), (33, 1, 272), (40, 3, 144), (5, 2, 2048)):
+        offsets, rows = routed(tokens, 1, experts, seed=fan_in)
+        x, w = scaled_rows(tokens, fan_in, seed=3), scaled_weights(experts, fan_out, fan_in, seed=4)
+        y = ns.ns_experts_product_scaled(*x, *w, offsets, rows, dtype=dtype)
+        assert "tile=32x32, k by 4 groups" in ns.ns_query_last_config()
+        check_product(y, x, w, offsets, rows, dtype)
+        assert torch.equal(y, ns.ns_experts_product_scaled(*x, *w, offsets, rows, dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_groups_of_waves_read_no_scale_but_their_own(dtype):
+    # five blocks to four groups: behind a row's last scale are the next row's, behind w's last the next expert's
+    x, w = scaled_rows(34, 640, seed=5), scaled_weights(2, 64, 640, seed=6)
+    offsets = torch.tensor([0, 33, 34], dtype=torch.int32, device=device())
+    want = ns.ns_experts_product_scaled(*x, *w, offsets, dtype=dtype)
+    x.scales.view(torch.uint8)[1::2] = 255
+    w.scales.view(torch.uint8)[1] = 255
+    y = torch.full_like(want, 7.0)
+    ends = offsets.clone()
+    ends[2] = 33
+    ns.ns_experts_product_scaled(*x, *w, ends, dtype=dtype, y=y)
+    assert torch.equal(y[0:33:2], want[0:33:2]) and bool(torch.isnan(y[1:33:2]).all()) and bool((y[33] == 7).all())
+
+
 def large_inputs(tokens, top_k, experts, fan_out, fan_in, gathered):
     offsets, rows = routed(tokens, top_k, experts, seed=tokens, spread=0.4)
     n = tokens * top_k
