@@ -651,6 +651,10 @@ long long most_row_tiles(const ScaledArgs& g, int bm) {
 //                 experts of 128 rows 11.7 (144) / 10.8 (288)
 //   small / few   1024 rows 9.3 (396) / 10.1; 128 rows, 4096 x 4096 11.2 (160) /
 //                 8.6; 128 experts of 16 rows 80 / 73, of 32 rows 92 / 103
+// For one matrix, whose tiles are known, fewer than 240 small ones are taken too where
+// those of 32 x 64 are more than one to a CU: 4096 x 14336, 128 rows (256 of them) 30 / 30, 129 rows (320) 31 / 58,
+// 200 rows 32 / 60; x 512, 200 rows 4.1 / 4.8; 2048 x 7168, 256 rows (256) 17 / 12, 300
+// rows (320) 17 / 18.
 // fp32 results go the same way, without the wide tile: tall / long 8 experts of 512
 // rows 29 / 36, of 256 rows 26 / 19; long / small 2048 rows 18 / 19, 1024 rows 16 / 14.
 //
@@ -676,7 +680,8 @@ ScaledTile choose_tile(int dtype, const ScaledArgs& g) {
     if (dtype == 1 && scale_blocks(g.fan_in) >= kWideLeastStages && tiles(kWide, kWide) >= 160) return TILE_WIDE;
     if (tiles(128, 256) >= 160) return TILE_TALL;
     if (tiles(128, 128) >= 160) return TILE_LONG;
-    if (tiles(64, 64) >= 240) return TILE_SMALL;
+    const bool rounds = g.experts == 1 && most_row_tiles(g, 32) * ((g.fan_out + 63) / 64) > kCUs;
+    if (tiles(64, 64) >= 240 || rounds) return TILE_SMALL;
   }
   if (most_row_tiles(g, 32) * ((g.fan_out + 31) / 32) <= kCUs && scale_blocks(g.fan_in) >= kSplitLeastBlocks) return TILE_SPLIT;
   return TILE_FEW;
