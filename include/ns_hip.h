@@ -489,8 +489,8 @@ int ns_experts_combine_backward(const void* dout, const void* y, const int32_t* 
 
 /*
  * ns_rms_norm - y = t rstd weight over the columns of each row, t = x + residual,
- * rstd = 1 / sqrt(mean(t^2) + eps).  Squares are added in fp32: where they pass 2^128 rstd is 0, and where
- * all of them are below 2^-150 the row counts as zeros.
+ * rstd = 1 / sqrt(mean(t^2) + eps).  Squares are added in fp32: where their sum
+ * passes 2^128 rstd is 0, and one below 2^-150 adds nothing.
  *
  *   x, residual
  *             [rows, cols] dtype, rows ldx and ldr elements apart; residual may
