@@ -489,8 +489,9 @@ int ns_experts_combine_backward(const void* dout, const void* y, const int32_t* 
 
 /*
  * ns_rms_norm - y = t rstd weight over the columns of each row, t = x + residual,
- * rstd = 1 / sqrt(mean(t^2) + eps).  Squares are added in fp32: where their sum
- * passes 2^128 rstd is 0, and one below 2^-150 adds nothing.
+ * rstd = 1 / sqrt(mean(t^2) + eps), in fp32.  Squares are added in 64 bits, so
+ * every finite row has one; below 2^-126 (rows of 2^126 and more) it is rounded to
+ * multiples of 2^-149, and where mean(t^2) + eps is below 2^-256 it is infinite.
  *
  *   x, residual
  *             [rows, cols] dtype, rows ldx and ldr elements apart; residual may

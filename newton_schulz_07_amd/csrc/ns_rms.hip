@@ -55,12 +55,19 @@ __device__ __forceinline__ Raw8<T> load_sum(const T* x, const T* r, int t, int i
   return a;
 }
 
-// rstd of a row from its threads' sums of squares, which are joined in 64 bits: y
-// goes on to 8 bits, where an error of the last places moves values across the
-// borders of the rounding.
+// The squares are added in 64 bits, which hold those of every finite value (in 32
+// bits a value of 2^64 or more made rstd 0, one below 2^-75 added nothing), and
+// joined in them: y goes on to 8 bits, where an error of the last places moves
+// values across the borders of the rounding.
+__device__ __forceinline__ double add_squares(const float (&f)[8], double s) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s = fma((double)f[e], (double)f[e], s);
+  return s;
+}
+// rstd of a row from its threads' sums of squares
 template <int WPR>
-__device__ __forceinline__ float rstd_of(float squares, const RmsNormArgs& g, double* red) {
-  double s = lanes_sum<64>((double)squares);
+__device__ __forceinline__ float rstd_of(double squares, const RmsNormArgs& g, double* red) {
+  double s = lanes_sum<64>(squares);
   if (WPR > 1) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
     __syncthreads();
@@ -88,13 +95,12 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rms_norm_kernel(const R
     Raw8<T> r[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) r[i] = load_sum<T, TPR, HOW>(x, res, t, i, g.cols);
-    float s = 0.0f;
+    double s = 0.0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       float f[8];
       unpack8(r[i], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(f[e], f[e], s);
+      s = add_squares(f, s);
     }
     const float rstd = rstd_of<WPR>(s, g, red[turn]);
     turn ^= 1;
@@ -124,11 +130,11 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RmsNormArgs g
   for (long long row = blockIdx.x; row < g.rows; row += gridDim.x) {
     const T* x = reinterpret_cast<const T*>(g.x) + row * g.ldx;
     const T* res = g.residual ? reinterpret_cast<const T*>(g.residual) + row * g.ldr : nullptr;
-    float s = 0.0f, f[8];
+    double s = 0.0;
+    float f[8];
     for (int i = 0; i < nv; ++i) {
       unpack8(load_sum<T, 1024, HOW>(x, res, t, i, g.cols), f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(f[e], f[e], s);
+      s = add_squares(f, s);
     }
     const float rstd = rstd_of<16>(s, g, red[turn]);
     turn ^= 1;

@@ -1,0 +1,68 @@
+"""Edges of the sublayer in 8 bits, on the GPU, against float64: the largest and the least magnitudes and scales, sizes
+at which a choice of tile changes, offsets that no routing makes.
+
+U and HALF are test_gpu_scaled's: half a step of fp32, and of a result's type, relative.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import newton_schulz_07_amd as ns
+from oracle import scaled as ref
+from tests.gpu_util import device, to64
+from tests.test_gpu_scaled import DTYPES, HALF, U, check_gradient, check_scaled, normal
+
+pytestmark = pytest.mark.gpu
+
+
+# -------------------------------------------------------------- RMS norm
+
+# every way a row is held, whole vectors and single columns
+NORM_COLS = [16, 5, 512, 1040, 1531, 2048, 2047, 4096, 8208, 16384, 16400, 32784, 33001]
+
+
+def of_magnitude(rows, cols, top, dtype, seed):
+    """Values between a quarter of top and top, of either sign."""
+    g = torch.Generator().manual_seed(seed)
+    v = (0.25 + 0.75 * torch.rand(rows, cols, generator=g)) * torch.sign(torch.rand(rows, cols, generator=g) - 0.5)
+    return (v.double() * top).float().to(dtype).to(device())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", NORM_COLS)
+@pytest.mark.parametrize("top,eps", [(3e38, 1e-6), (1e30, 1e-6), (1.5e19, 1e-6), (1e17, 0.0), (1e-19, 0.0), (1e-22, 0.0),
+                                     (1e-30, 0.0), (2e-38, 0.0)])
+def test_rms_norm_of_squares_that_fp32_does_not_hold(dtype, cols, top, eps):
+    x, w = of_magnitude(3, cols, top, dtype, seed=cols), 1 + 0.2 * normal(cols, seed=5)
+    eight = cols % 16 == 0
+    n = ns.ns_rms_norm(x, w, eps=eps, outputs="both" if eight else "same")
+    want, rstd = ref.rms_norm(to64(x), to64(w), eps)
+    # the sum of squares is off by cols 2^-53 at most, which is nothing; then one rounding, below 2^-126 to multiples of 2^-149
+    off = np.maximum(U * rstd, 2.0 ** -150) * (1 + 2.0 ** -20)
+    assert np.all(np.abs(to64(n.rstd) - rstd) <= off)
+    slack = 3 * U + (off / rstd)[:, None]  # two products, and rstd's own
+    assert np.all(np.abs(to64(n.y) - want) <= (HALF[dtype] + slack) * np.abs(want))
+    if eight:
+        check_scaled(n.q, n.scales, want, slack.max())
+
+
+@pytest.mark.parametrize("cols", NORM_COLS)
+def test_rms_norm_of_one_large_value(cols):
+    # one value whose square no fp32 holds: the row's others are what they are beside it, not zeros
+    x = normal(2, cols, seed=cols)
+    x[1, cols // 2] = -2.0 ** 100
+    y, want = to64(ns.ns_rms_norm(x).y), ref.rms_norm(to64(x))[0]
+    assert np.all(np.abs(y - want) <= 4 * U * np.abs(want)) and y[1].all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", NORM_COLS)
+@pytest.mark.parametrize("top", [1.5e19, 1e25, 1e-22])
+def test_rms_norm_gradient_of_squares_that_fp32_does_not_hold(dtype, cols, top):
+    x, w = of_magnitude(3, cols, top, dtype, seed=cols), 1 + 0.2 * normal(cols, seed=5)
+    rstd = ns.ns_rms_norm(x, w, eps=0.0).rstd
+    dy = normal(3, cols, seed=7, dtype=dtype)
+    dx, dw = ns.ns_rms_norm_backward(dy, x, w, rstd)
+    check_gradient(dx, dw, dy, x, w, rstd, None)
+    assert dx.any() and dw.any()
