@@ -390,7 +390,8 @@ hipError_t launch_tiles(ExpertsArgs g, hipStream_t st) {
   } else {
     // sum of ceil(c / BM) over at most min(experts, n_rows) non-empty experts
     const long long some = g.experts < g.n_rows ? g.experts : g.n_rows;
-    grid = ((g.n_rows + some * (BM - 1)) / BM) * tiles_n;
+    g.most_row_tiles = (int)((g.n_rows + some * (BM - 1)) / BM);
+    grid = g.most_row_tiles * tiles_n;
     grid = (grid + 7) / 8 * 8;  // every XCD reaches its last live tile
   }
   if (grid <= 0) return hipSuccess;

@@ -374,10 +374,10 @@ __global__ __launch_bounds__(256, 1) void experts_scaled_wide_kernel(const Scale
   __syncthreads();
   struct {
     const int* offsets;
-    int experts, n_rows;
-  } const ex{offsets, g.experts, g.n_rows};
+    int experts, n_rows, most_row_tiles;
+  } const ex{offsets, g.experts, g.n_rows, g.most_row_tiles};
   int upto;
-  const int row_tiles = min(count_tiles(ex, kWide, &upto), g.most_row_tiles), total = row_tiles * tiles_n;
+  const int total = count_tiles(ex, kWide, &upto) * tiles_n;
   // each XCD takes a contiguous run of the tiles, its workgroups one after another
   const int xcd = blockIdx.x % 8, per = total / 8, rem = total % 8;
   const int first_tile = xcd * per + min(xcd, rem), tiles = per + (xcd < rem ? 1 : 0);
@@ -607,12 +607,17 @@ __global__ __launch_bounds__(256, 1) void experts_scaled_wide_kernel(const Scale
   wait_vm_lgkm0<0>();  // (loads of nothing may still be on their way to the LDS)
 }
 
+// Row tiles of bm that n_rows rows can make: the sum of ceil(c / bm) over at most min(experts, n_rows) experts with rows.
+long long most_row_tiles(const ScaledArgs& g, int bm) {
+  return (g.n_rows + (long long)std::min(g.experts, g.n_rows) * (bm - 1)) / bm;
+}
+
 template <typename T, int BM, int BN, int WM, int WN, int ST, int OCC, int KG>
 hipError_t launch_tiles(ScaledArgs g, hipStream_t st) {
   const long long tiles_n = (g.fan_out + BN - 1) / BN;
-  // sum of ceil(c / BM) over at most min(experts, n_rows) non-empty experts
-  const long long some = g.experts < g.n_rows ? g.experts : g.n_rows;
-  long long grid = ((g.n_rows + some * (BM - 1)) / BM) * tiles_n;
+  const long long most = most_row_tiles(g, BM);
+  g.most_row_tiles = (int)most;
+  long long grid = most * tiles_n;
   grid = (grid + 7) / 8 * 8;  // every XCD reaches its last live tile
   if (grid <= 0) return hipSuccess;
   if (grid * (WM * WN * KG * 64) >= 1ll << 32) return hipErrorInvalidValue;  // a launch holds fewer threads
@@ -632,11 +637,6 @@ hipError_t launch_tiles(ScaledArgs g, hipStream_t st) {
 #define NS_SCALED_FEW 32, 64, 1, 2, 4, 3, 1
 #define NS_SCALED_SPLIT 32, 32, 1, 1, 4, 1, 4
 enum ScaledTile { TILE_WIDE, TILE_TALL, TILE_LONG, TILE_SMALL, TILE_FEW, TILE_SPLIT };
-
-// Row tiles of bm that n_rows rows can make: the sum of ceil(c / bm) over at most min(experts, n_rows) experts with rows.
-long long most_row_tiles(const ScaledArgs& g, int bm) {
-  return (g.n_rows + (long long)std::min(g.experts, g.n_rows) * (bm - 1)) / bm;
-}
 
 // The largest tile that makes about 160 workgroups (240 of the small ones, of which
 // three share a CU): a large tile reads less for each product, a small one fills

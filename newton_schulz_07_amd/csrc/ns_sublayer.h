@@ -187,6 +187,7 @@ struct ExpertsArgs {
   long long ldx;
   int n_x, n_rows, experts, fan_out, fan_in;
   bool stream;
+  int most_row_tiles;  // of the tile that is launched, for offsets that ascend (set at the launch)
 };
 // What launch_experts runs, for ns_query_last_config: a format of the type's
 // name, n_rows, experts, fan_out and fan_in.

@@ -24,8 +24,9 @@ __device__ __forceinline__ void expert_rows(const int* offsets, int e, int exper
   *begin = b;
   *count = c > b ? c - b : 0;
 }
-// (Offsets that ascend make fewer than 2^27.  Where experts claim the same rows again
-// and again the count stops here, so that it never turns negative.)
+// Offsets that ascend make at most g.most_row_tiles, which the launch has a grid for:
+// times the column tiles that is below 2^31.  Where experts claim the same rows again
+// and again the sum itself stops at 2^30, so that it never turns negative.
 constexpr int kMostTiles = (1 << 30) - 1;
 template <typename G> __device__ __forceinline__ int count_tiles(const G& g, int bm, int* upto) {
   const int lane = threadIdx.x & 63, per = (g.experts + 63) / 64;
@@ -41,7 +42,7 @@ template <typename G> __device__ __forceinline__ int count_tiles(const G& g, int
     if (lane >= o) n = min(n + u, kMostTiles);
   }
   *upto = n;
-  return __builtin_amdgcn_readlane(n, 63);
+  return min(__builtin_amdgcn_readlane(n, 63), g.most_row_tiles);
 }
 template <typename G> __device__ __forceinline__ Tile find_tile(const G& g, int bm, int upto, int q) {
   const int per = (g.experts + 63) / 64;

@@ -66,3 +66,27 @@ def test_rms_norm_gradient_of_squares_that_fp32_does_not_hold(dtype, cols, top):
     dx, dw = ns.ns_rms_norm_backward(dy, x, w, rstd)
     check_gradient(dx, dw, dy, x, w, rstd, None)
     assert dx.any() and dw.any()
+
+
+# --------------------------------------------------- the experts' product
+
+
+@pytest.mark.parametrize("eight", [True, False])
+def test_offsets_whose_tiles_of_all_columns_pass_32_bits(eight):
+    # 512 of 1024 experts claim all rows: 2^17 row tiles of 2^14 column tiles.  Every row is one of theirs and is written.
+    experts, rows, fan_out, fan_in = 1024, 8192, 1 << 20, 16 if eight else 8
+    offsets = torch.tensor([0, rows] * (experts // 2) + [0], dtype=torch.int32, device=device())
+    guard = torch.full((rows + 64, fan_out), 7.0, dtype=torch.bfloat16, device=device())
+    if eight:
+        def ones(*shape, code, dtype):
+            return torch.full(shape, code, dtype=torch.uint8, device=device()).view(dtype)
+        x, w = ((ones(*s, fan_in, code=0x38, dtype=torch.float8_e4m3fn), ones(*b, 1, code=127, dtype=torch.float8_e8m0fnu))
+                for s, b in (((rows,), (rows,)), ((experts, fan_out), (experts, fan_out // 128))))
+        ns.ns_experts_product_scaled(*x, *w, offsets, y=guard[:rows])
+    else:
+        x, w = (torch.ones(*s, fan_in, dtype=torch.bfloat16, device=device()) for s in ((rows,), (experts, fan_out)))
+        ns.ns_experts_product(x, w, offsets, y=guard[:rows])
+    low, high = guard[:rows].aminmax()
+    assert low.item() == high.item() == fan_in and bool((guard[rows:] == 7).all())
+    del x, w, guard
+    torch.cuda.empty_cache()
