@@ -107,9 +107,11 @@ enum {
  * A is mirrored too, except on large bf16 stacks, where it is kept as its
  * lower block triangle and the polynomial reads the rest transposed.
  * The workspace (ns_workspace_bytes) is allocated on first use per
- * (device, stream) and grown when needed.  Growing allocates a new buffer
- * without synchronising; the replaced one stays allocated (work queued
- * earlier may still use it) until ns_release_workspace.  Once the workspace
+ * (device, stream) and grown when needed.  Growing allocates a new buffer of
+ * at least twice the old one's size (of the call's own, where there is no room
+ * for that) without synchronising; the replaced one stays allocated (work queued
+ * earlier may still use it) until ns_release_workspace.  Where there is room, a
+ * stream thus holds at most four times what its largest call needs.  Once the workspace
  * of (device, stream) is at least this call's size, a call makes no
  * allocation and no synchronisation: it enqueues only kernels (and, in place
  * with an odd step count, one device copy), so it can be captured into a
@@ -580,7 +582,8 @@ int ns_experts_product_scaled(const void* x, const uint8_t* x_scales, int64_t n_
  * kept in 8 bits: dw[e] = sum over its rows of dy[i]^T x[rows[i]], dy [n_rows,
  * fan_out] and dw [experts, fan_out, fan_in] in dtype.  offsets is not NULL.  x is
  * restored in dtype in library workspace (n_x rows, or n_rows without rows), which
- * is less than 2 GiB where there are rows, and has no such limit without.
+ * is less than 2 GiB where there are rows, and has no such limit without; it stays
+ * allocated as every workspace does (ns_orthogonalize, ns_release_workspace).
  */
 int ns_experts_weight_grad_scaled(const void* dy, const void* x, const uint8_t* x_scales,
                                   int64_t n_x, const int32_t* rows, const int32_t* offsets,

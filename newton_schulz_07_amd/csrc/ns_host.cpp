@@ -81,8 +81,10 @@ struct Ws {
 };
 std::mutex g_ws_mu;  // the containers below (taken after an `enqueueing`, never before one)
 std::map<std::pair<int, void*>, Ws> g_ws;
-// Buffers replaced by a larger one.  Work queued earlier may still read
-// them, so they are freed only by ns_release_workspace.
+// Buffers replaced by a larger one.  Work queued earlier and captured graphs may
+// still read them, so they are freed only by ns_release_workspace.  A buffer is at
+// least twice the one that it replaces, if there is room: all of a stream's replaced
+// ones together are no larger than its present one, however slowly calls grow.
 std::vector<std::pair<int, void*>> g_ws_retired;
 std::atomic<int64_t> g_ws_allocs{0};
 }  // namespace
@@ -99,9 +101,12 @@ int get_workspace(hipStream_t st, size_t bytes, Workspace* out) {
   std::unique_lock<std::mutex> held(w.enqueueing);
   if (w.bytes < bytes) {
     void* p = nullptr;
-    if (hipMalloc(&p, bytes) != hipSuccess || p == nullptr) {
+    size_t size = w.bytes > bytes / 2 ? 2 * w.bytes : bytes;
+    for (;;) {
+      if (hipMalloc(&p, size) == hipSuccess && p != nullptr) break;
       (void)hipGetLastError();
-      return fail(NS_ERR_OOM, "workspace allocation of " + std::to_string(bytes) + " bytes failed");
+      if (size == bytes) return fail(NS_ERR_OOM, "workspace allocation of " + std::to_string(bytes) + " bytes failed");
+      size = bytes;  // no room for twice as much: as much as is needed
     }
     ++g_ws_allocs;
     if (w.ptr != nullptr) {
@@ -109,7 +114,7 @@ int get_workspace(hipStream_t st, size_t bytes, Workspace* out) {
       g_ws_retired.emplace_back(dev, w.ptr);
     }
     w.ptr = p;
-    w.bytes = bytes;
+    w.bytes = size;
   }
   out->ptr = static_cast<char*>(w.ptr);
   out->held = std::move(held);

@@ -90,3 +90,20 @@ def test_offsets_whose_tiles_of_all_columns_pass_32_bits(eight):
     assert low.item() == high.item() == fan_in and bool((guard[rows:] == 7).all())
     del x, w, guard
     torch.cuda.empty_cache()
+
+
+# -------------------------------------------------------- weight gradient
+
+
+def test_a_batch_that_grows_slowly_takes_few_workspaces():
+    # the restored rows of 64 batches, the last one 4.2 times the first: two doublings and the first
+    w_rows = [200 + 10 * i for i in range(64)]
+    x, dy = ns.ns_quantize(normal(w_rows[-1], 512, seed=1)), normal(w_rows[-1], 16, seed=2)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        before = ns.ns_workspace_allocations()
+        for n in w_rows:
+            offsets = torch.tensor([0, n], dtype=torch.int32, device=device())
+            ns.ns_experts_weight_grad_scaled(dy[:n], x.q[:n], x.scales[:n], offsets)
+        assert ns.ns_workspace_allocations() - before <= 4
+        torch.cuda.synchronize()
