@@ -650,7 +650,25 @@ enum ScaledTile { TILE_WIDE, TILE_TALL, TILE_LONG, TILE_SMALL, TILE_FEW, TILE_SP
 //   long / small  2048 rows 11.5 (198) / 13.4, 1024 rows 10.7 (102) / 9.3; 8
 //                 experts of 128 rows 11.7 (144) / 10.8 (288)
 //   small / few   1024 rows 9.3 (396) / 10.1; 128 rows, 4096 x 4096 11.2 (160) /
-//                 8.6; 128 experts of 16 rows 80 / 73, of 32 rows 92 / 103
+//                 8.6; 128 experts of 16 rows 80 / 71
+// That holds where an expert has rows for much of a tile.  With fewer every expert has one
+// tile whatever its height, so that many experts make many tiles, and what a tall one does
+// for no rows counts.  By rows of each expert (E of 1536 x 2048; K: 64 of 1280 x 512), us:
+//   bf16   16: E = 128 wide 81, tall 80, small 80, few 71    64: 53, 48, 42, 38   K: 21, 17, 13, 13
+//          20:              84       80        83      79        52  47  45  41      22  17  13  14
+//          28:              87       87        90      96        53  49  46  45      22  18  14  18
+//          32:              87       91        93     103        53  49  47  50      22  18  14  18
+//          48:              90       96       103     131        55  51  54  65      22  19  16  23
+//   fp32   20: E = 128 tall 94, small 91, few 90             64: 56, 46, 46       K: 22, 15, 17
+//          32:             104        98     110                 58  52  55          22  16  21
+//          47:             116       111     131                 60  59  71          23  19  26
+//          64:             121       128     154                 63  66  80          24  21  30
+//   long, small: 32 of 1536 x 2048, 20 rows 27 / 25 (fp32 35 / 26), 24 of them 23 / 17 (32 / 19);
+//                one to a CU, 8 of 4096 x 14336 84 / 92
+//   few, small, 17 to 20 rows: 64 of 1280 x 512 14 / 13, 512 of 256 x 512 28 / 22, 128 of
+//                2048 x 768 48 / 52, 256 of 512 x 1024 33 / 35, 4 of 24576 x 4096 71 / 83
+// So with up to kFewRows rows 32 x 64 is taken there (from kFewLeastBlocks blocks of k on),
+// and otherwise 64 x 64 with fewer than kTallRows.
 // For one matrix, whose tiles are known, fewer than 240 small ones are taken too where
 // those of 32 x 64 are more than one to a CU: 4096 x 14336, 128 rows (256 of them) 30 / 30, 129 rows (320) 31 / 58,
 // 200 rows 32 / 60; x 512, 200 rows 4.1 / 4.8; 2048 x 7168, 256 rows (256) 17 / 12, 300
@@ -671,15 +689,20 @@ enum ScaledTile { TILE_WIDE, TILE_TALL, TILE_LONG, TILE_SMALL, TILE_FEW, TILE_SP
 // (Two groups, two workgroups to a CU: 17 in the first case and 4 % less at 1536 x 512;
 // 32 x 64 by four groups 23; six or eight groups with fewer stages 16 and 22.)
 constexpr int kCUs = 256, kSplitLeastBlocks = 4;
+constexpr int kFewRows = 20, kFewLeastBlocks = 5, kTallRows[2] = {48, 32};  // (fp32 results, bf16)
 ScaledTile choose_tile(int dtype, const ScaledArgs& g) {
   const int rows = g.n_rows / g.experts;  // an expert's, on average
   auto tiles = [&](int bm, int bn) {
     return ((long long)g.n_rows / bm + std::min(g.experts, g.n_rows) / 2.0) * ((g.fan_out + bn - 1) / bn);
   };
   if (rows > 16) {
-    if (dtype == 1 && scale_blocks(g.fan_in) >= kWideLeastStages && tiles(kWide, kWide) >= 160) return TILE_WIDE;
-    if (tiles(128, 256) >= 160) return TILE_TALL;
-    if (tiles(128, 128) >= 160) return TILE_LONG;
+    const bool many = g.experts > 1, few = many && rows <= kFewRows;
+    if (tiles(128, 256) >= 160) {
+      if (few && scale_blocks(g.fan_in) >= kFewLeastBlocks) return TILE_FEW;
+      if (many && rows < kTallRows[dtype]) return TILE_SMALL;
+      return dtype == 1 && scale_blocks(g.fan_in) >= kWideLeastStages && tiles(kWide, kWide) >= 160 ? TILE_WIDE : TILE_TALL;
+    }
+    if (tiles(128, 128) >= 160) return few && g.experts * ((g.fan_out + 127) / 128) > kCUs ? TILE_SMALL : TILE_LONG;
     const bool rounds = g.experts == 1 && most_row_tiles(g, 32) * ((g.fan_out + 63) / 64) > kCUs;
     if (tiles(64, 64) >= 240 || rounds) return TILE_SMALL;
   }

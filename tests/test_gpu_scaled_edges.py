@@ -11,7 +11,8 @@ import torch
 import newton_schulz_07_amd as ns
 from oracle import scaled as ref
 from tests.gpu_util import device, to64
-from tests.test_gpu_scaled import DTYPES, HALF, U, check_gradient, check_scaled, normal
+from tests.test_gpu_scaled import (DTYPES, HALF, U, check_gradient, check_product, check_scaled, normal, routed,
+                                   scaled_rows, scaled_weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -90,6 +91,25 @@ def test_offsets_whose_tiles_of_all_columns_pass_32_bits(eight):
     assert low.item() == high.item() == fan_in and bool((guard[rows:] == 7).all())
     del x, w, guard
     torch.cuda.empty_cache()
+
+
+# experts, fan_out, fan_in; and by rows of each expert the tile of bf16 and of fp32 results: 64 experts of 1296 columns have
+# more than 160 tiles of 128 x 256 whatever their rows, 32 of 1040 more than 160 of 128 x 128, 16 of 2048 one to a CU
+BORDERS = [(64, 1296, 528, {16: "32x64", 17: "32x64", 20: "32x64", 21: "64x64", 31: "64x64", 32: ("256x256", "64x64"),
+                            47: ("256x256", "64x64"), 48: ("256x256", "128x256")}),
+           (64, 1296, 272, {16: "32x64", 17: "64x64", 31: "64x64", 32: ("128x256", "64x64"), 48: "128x256"}),
+           (32, 1040, 272, {17: "64x64", 20: "64x64", 21: "128x128"}), (16, 2048, 272, {20: "128x128", 21: "128x128"})]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("experts,fan_out,fan_in,rows,tile",
+                         [(e, n, k, r, t) for e, n, k, tiles in BORDERS for r, t in tiles.items()])
+def test_product_at_the_rows_where_its_tile_changes(dtype, experts, fan_out, fan_in, rows, tile):
+    offsets, numbers = routed(experts * rows // 2, 2, experts, seed=rows, spread=0.4)
+    x, w = scaled_rows(experts * rows // 2, fan_in, seed=1), scaled_weights(experts, fan_out, fan_in, seed=2)
+    y = ns.ns_experts_product_scaled(*x, *w, offsets, numbers, dtype=dtype)
+    assert ns.ns_query_last_config().endswith("tile=" + (tile if isinstance(tile, str) else tile[dtype == torch.float32]))
+    check_product(y, x, w, offsets, numbers, dtype)
 
 
 # -------------------------------------------------------- weight gradient
