@@ -580,7 +580,8 @@ int ns_experts_product_scaled(const void* x, const uint8_t* x_scales, int64_t n_
 /*
  * ns_experts_weight_grad_scaled - ns_experts_weight_grad from rows x that were
  * kept in 8 bits: dw[e] = sum over its rows of dy[i]^T x[rows[i]], dy [n_rows,
- * fan_out] and dw [experts, fan_out, fan_in] in dtype.  offsets is not NULL.  x is
+ * fan_out] and dw [experts, fan_out, fan_in] in dtype.  offsets may be NULL for one
+ * expert that has all rows, as in the product (a linear layer's gradient).  x is
  * restored in dtype in library workspace (n_x rows, or n_rows without rows), which
  * is less than 2 GiB where there are rows, and has no such limit without; it stays
  * allocated as every workspace does (ns_orthogonalize, ns_release_workspace).

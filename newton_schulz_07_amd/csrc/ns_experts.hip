@@ -97,7 +97,12 @@ __global__ __launch_bounds__(WM* WN * 64, (OCC * WM * WN + 3) / 4) void experts_
     rect_decode(q, tiles_m, tiles_n, tl.tile, tj);
     i0 = tl.tile * BM;
     j0 = tj * BN;
-    expert_rows(g.offsets, tl.expert, g.experts, g.n_rows, &tl.begin, &tl.count);
+    if (g.offsets != nullptr) {
+      expert_rows(g.offsets, tl.expert, g.experts, g.n_rows, &tl.begin, &tl.count);
+    } else {
+      tl.begin = 0;
+      tl.count = g.n_rows;
+    }
     tl.begin = __builtin_amdgcn_readfirstlane(tl.begin);
     tl.count = __builtin_amdgcn_readfirstlane(tl.count);
   } else {

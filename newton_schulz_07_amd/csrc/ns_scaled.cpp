@@ -275,7 +275,7 @@ int ns_experts_weight_grad_scaled(const void* dy, const void* x, const uint8_t* 
         return fail(NS_ERR_INVALID_ARG, "x read through rows must hold less than 2 GiB in dtype");
     }
     if (int s = check_opt4(offsets, "offsets")) return s;
-    if (offsets == nullptr) return fail(NS_ERR_INVALID_ARG, "offsets is NULL");
+    if (offsets == nullptr && experts != 1) return fail(NS_ERR_INVALID_ARG, "offsets is NULL: only one expert can have all rows");
     if (int s = check_ptr(dw, "dw")) return s;
     const Span out[] = {{dw, experts * fan_out * fan_in * es, "dw"}};
     const Span in[] = {{dy, n_rows * fan_out * es, "dy"}, {x, n_rows ? (size_t)(n_x * fan_in) : 0, "x"},

@@ -182,7 +182,7 @@ struct ExpertsArgs {
   const void* dy;      // [n_rows, fan_out] (gradients)
   const void* w;       // [experts, fan_out, fan_in] (product, input gradient)
   void* out;
-  const int* offsets;  // [experts + 1]
+  const int* offsets;  // [experts + 1], or null (weight gradient): one expert has all rows
   const int* rows;     // [n_rows], or null: row i of x
   long long ldx;
   int n_x, n_rows, experts, fan_out, fan_in;

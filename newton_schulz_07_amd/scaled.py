@@ -224,18 +224,20 @@ def ns_experts_product_scaled(x, x_scales, w, w_scales, offsets=None, rows=None,
     return y
 
 
-def ns_experts_weight_grad_scaled(dy, x, x_scales, offsets, rows=None, dw=None):
+def ns_experts_weight_grad_scaled(dy, x, x_scales, offsets=None, rows=None, dw=None):
     """dw[e] = dy[i].T @ x[rows[i]] over expert e's sorted rows, from x kept in 8 bits: [experts, fan_out, fan_in] in
-    dy's type (bf16 or fp32), zero for an expert without rows."""
+    dy's type (bf16 or fp32), zero for an expert without rows.  Without offsets there is one expert, which has all rows,
+    and dw is [fan_out, fan_in]: a linear layer."""
     n_x, fan_in, n_rows = _scaled_rows(x, x_scales, rows)
-    _dense(offsets, "offsets", x, torch.int32)
-    if offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError("offsets must be [experts + 1]")
+    if offsets is not None:
+        _dense(offsets, "offsets", x, torch.int32)
+        if offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError("offsets must be [experts + 1]")
     if dy.dim() != 2:
         raise ValueError("dy must be [n_rows, fan_out]")
-    experts, fan_out = offsets.numel() - 1, dy.shape[1]
+    experts, fan_out = 1 if offsets is None else offsets.numel() - 1, dy.shape[1]
     _dense(dy, "dy", x, None, (n_rows, fan_out))
-    dw = _out(dw, "dw", x, dy.dtype, (experts, fan_out, fan_in))
+    dw = _out(dw, "dw", x, dy.dtype, (fan_out, fan_in) if offsets is None else (experts, fan_out, fan_in))
     _call("ns_experts_weight_grad_scaled", x, dy.data_ptr(), x.data_ptr(), x_scales.data_ptr(), n_x, _ptr(rows),
-          offsets.data_ptr(), dw.data_ptr(), n_rows, experts, fan_out, fan_in, _code(dy.dtype))
+          _ptr(offsets), dw.data_ptr(), n_rows, experts, fan_out, fan_in, _code(dy.dtype))
     return dw

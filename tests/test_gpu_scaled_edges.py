@@ -12,7 +12,7 @@ import newton_schulz_07_amd as ns
 from oracle import scaled as ref
 from tests.gpu_util import device, to64
 from tests.test_gpu_scaled import (DTYPES, HALF, U, check_gradient, check_product, check_scaled, normal, routed,
-                                   scaled_rows, scaled_weights)
+                                   rows64, scaled_rows, scaled_weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +127,23 @@ def test_a_batch_that_grows_slowly_takes_few_workspaces():
             ns.ns_experts_weight_grad_scaled(dy[:n], x.q[:n], x.scales[:n], offsets)
         assert ns.ns_workspace_allocations() - before <= 4
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,fan_out,fan_in", [(1, 16, 16), (33, 48, 144), (700, 272, 400), (5000, 2064, 528)])
+@pytest.mark.parametrize("gathered", [True, False])
+def test_weight_gradient_of_a_linear_layer(dtype, n, fan_out, fan_in, gathered):
+    offsets, rows = routed(n, 1, 1, seed=n)
+    rows = rows.flip(0).contiguous() if gathered else None
+    x, dy = scaled_rows(n, fan_in, seed=1), normal(n, fan_out, seed=2, dtype=dtype)
+    dw = ns.ns_experts_weight_grad_scaled(dy, *x, rows=rows)
+    assert dw.shape == (fan_out, fan_in) and dw.dtype == dtype
+    assert torch.equal(dw, ns.ns_experts_weight_grad_scaled(dy, *x, offsets, rows)[0])
+    x64 = rows64(x) if rows is None else rows64(x)[rows.long()]
+    want = dy.double().T @ x64
+    slack = 2 * n * U * (dy.double().abs().T @ x64.abs())
+    assert bool(((dw.double() - want).abs() <= HALF[dtype] * want.abs() + slack).all())
+    out = torch.full_like(dw, 7.0)
+    assert ns.ns_experts_weight_grad_scaled(dy[:0], x.q[:0], x.scales[:0], dw=out) is out and not out.any()
+    with pytest.raises(ValueError):
+        ns.ns_experts_weight_grad_scaled(dy, *x, rows=rows, dw=torch.empty(2, fan_out, fan_in, dtype=dtype, device=device()))
