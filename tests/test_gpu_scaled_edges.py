@@ -69,6 +69,20 @@ def test_rms_norm_gradient_of_squares_that_fp32_does_not_hold(dtype, cols, top):
     assert dx.any() and dw.any()
 
 
+@pytest.mark.parametrize("cols", [1040, 1531, 4096, 8191, 16400, 33001])
+def test_rms_norm_weight_gradient_joins_rows_as_a_tree(cols):
+    # 64 rows, a block of threads to each: one term of 1 and 63 of 2^-25, which nothing is left of when they are added to
+    # it one after another.  In a tree a term passes 6 additions, and 2 roundings before: 8 halves of a step of the sum.
+    x = torch.ones(64, cols, device=device())
+    x[:, ::3] = -1
+    dy = torch.full((64, cols), 2.0 ** -25, device=device())
+    dy[5] = 1.0
+    w = torch.ones(cols, device=device())
+    dw = ns.ns_rms_norm_backward(dy, x, w, torch.ones(64, device=device()))[1]
+    want = (1 + 63 * 2.0 ** -25) * to64(x[0])
+    assert np.all(np.abs(to64(dw) - want) <= 8 * U * np.abs(want))
+
+
 # --------------------------------------------------- the experts' product
 
 
