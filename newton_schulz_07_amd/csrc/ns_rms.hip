@@ -158,7 +158,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RmsNormArgs g
 template <typename T, int TPR, int VPT, int HOW>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rms_norm_backward_kernel(const RmsNormGradArgs g) {
   constexpr int WPR = TPR / 64, RPB = TPR == 64 ? 4 : 1;
-  __shared__ float2 red[2][WPR];
+  __shared__ float red[2][WPR];
   __shared__ float part[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? TPR * VPT * 8 : 1];
   const int t = threadIdx.x % TPR, rl = threadIdx.x / TPR;
   const float inv_n = 1.0f / (float)g.cols;
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rms_norm_backward_kerne
         aw[i][e] = fmaf(fd[e], th, aw[i][e]);
       }
     }
-    c = row_sum<WPR>(c, 0.0f, red[turn]).x * inv_n;
+    c = row_sum<WPR>(c, red[turn]) * inv_n;
     turn ^= 1;
     if (g.dx) {
       T* dx = reinterpret_cast<T*>(g.dx) + row * (long long)g.cols;
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rms_norm_backward_kerne
 // row of `partials`, which it alone touches.
 template <typename T, int HOW>
 __global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RmsNormGradArgs g) {
-  __shared__ float2 red[2][16];
+  __shared__ float red[2][16];
   const int t = threadIdx.x, nv = (g.cols + 8191) / 8192;
   const float inv_n = 1.0f / (float)g.cols;
   float* out = g.partials ? g.partials + (size_t)blockIdx.x * partials_ld(g.cols) : nullptr;
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RmsN
       }
     }
     first = false;
-    c = row_sum<16>(c, 0.0f, red[turn]).x * inv_n;
+    c = row_sum<16>(c, red[turn]) * inv_n;
     turn ^= 1;
     if (g.dx == nullptr) continue;
     T* dx = reinterpret_cast<T*>(g.dx) + row * (long long)g.cols;

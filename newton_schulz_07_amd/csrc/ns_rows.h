@@ -84,6 +84,20 @@ __device__ __forceinline__ float2 row_sum(float a, float b, float2* red) {
   return make_float2(a, b);
 }
 
+// The same of one number.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float a, float* red) {
+  a = lanes_sum<64>(a);
+  if (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = a;
+    __syncthreads();
+    a = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) a += red[w];
+  }
+  return a;
+}
+
 __device__ __forceinline__ void store_param(void* p, int pdt, int c, float v) {
   if (p == nullptr) return;
   if (pdt == 1) reinterpret_cast<bf16*>(p)[c] = (bf16)v;

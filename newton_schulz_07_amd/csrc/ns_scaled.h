@@ -62,7 +62,6 @@ struct QuantizeArgs {
   uint8_t *q, *scales;
   long long ldx;
   unsigned rows, cols, blocks;  // blocks: of a row
-  bool stream;
 };
 struct QuantizeWeightsArgs {
   const void* w;                  // [experts, fan_out, fan_in]
@@ -75,7 +74,6 @@ struct DequantizeArgs {
   void* x;
   unsigned rows, cols, blocks;    // all matrices' rows
   unsigned matrix_rows, matrix_blocks;  // of one matrix, and its blocks of rows (weights)
-  bool stream;
 };
 hipError_t launch_quantize(int dtype, const QuantizeArgs& g, hipStream_t st);
 hipError_t launch_quantize_weights(int dtype, const QuantizeWeightsArgs& g, hipStream_t st);
