@@ -566,8 +566,11 @@ int ns_dequantize(const void* q, const uint8_t* scales, void* x, int64_t matrice
  * eight neighbouring products at a time and cut each off at 2^-13 of the largest
  * one's power of two, everything else in fp32: at most 2^-10 of the sum of the
  * eights' largest products, and 1.5e-5 of the result (root mean square) in rows
- * of normal values.  Results in fp32 are fp32 sums of exact products of x and w as
- * ns_dequantize gives them in bf16, at half the rate.  A launch of 2^32 threads or
+ * of normal values.  Where large products cancel that may be more than the result's
+ * rounding.  Results in fp32 are fp32 sums of exact products of x and w as
+ * ns_dequantize gives them in bf16 (infinite past its largest value, which takes a
+ * scale of 2^120 or more), at half the rate; rounded, they are the bf16 results of
+ * exact products.  A launch of 2^32 threads or
  * more is an error: 2^30 rows and more, where it goes by tiles of 128 rows (fp32, or
  * fan_in of at most 384).
  */

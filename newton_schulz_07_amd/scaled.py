@@ -202,8 +202,9 @@ def ns_experts_product_scaled(x, x_scales, w, w_scales, offsets=None, rows=None,
 
     x, x_scales: 8-bit rows [n_x, fan_in]; w, w_scales: 8-bit weights [experts, fan_out, fan_in]; offsets, rows: int32,
     from ns_route (rows None: x is sorted already).  Without offsets there is one expert, which has all rows, and w may
-    be [fan_out, fan_in]: a linear layer.  Returns y [n_rows, fan_out] in dtype (bf16, or fp32: exact products, at half
-    the rate); rows that no expert has are not written.  With ns_quantize_weights' transposed weights and dy in 8 bits
+    be [fan_out, fan_in]: a linear layer.  Returns y [n_rows, fan_out] in dtype: bf16, from products that are cut off at
+    2^-13 of the largest of eight neighbours, or fp32, from exact ones, at half the rate (to be had in bf16 by rounding
+    them: where large products cancel).  Rows that no expert has are not written.  With ns_quantize_weights' transposed weights and dy in 8 bits
     it is the gradient of x, row by row.
     """
     n_x, fan_in, n_rows = _scaled_rows(x, x_scales, rows)

@@ -11,10 +11,20 @@ import torch
 import newton_schulz_07_amd as ns
 from oracle import scaled as ref
 from tests.gpu_util import device, to64
-from tests.test_gpu_scaled import (DTYPES, HALF, U, check_gradient, check_product, check_scaled, normal, routed,
-                                   rows64, scaled_rows, scaled_weights)
+from tests.test_gpu_scaled import (DTYPES, HALF, U, check_gradient, check_product, check_scaled, large_inputs, normal,
+                                   routed, rows64, scaled_rows, scaled_weights, weights64)
 
 pytestmark = pytest.mark.gpu
+
+
+def bound(x, w, dtype):
+    """How far a product of x [rows, k] and w [columns, k] may be off: its rounding, k additions in fp32 and, in bf16
+    results, eights whose products are each cut off at 2^-13 of the largest one's power of two."""
+    slack = 2 * x.shape[1] * U * (x.abs() @ w.abs().T) + HALF[dtype] * (x @ w.T).abs()
+    if dtype == torch.bfloat16:
+        for k in range(0, x.shape[1], 8):
+            slack += 2.0 ** -10 * (x[:, None, k:k + 8] * w[None, :, k:k + 8]).abs().amax(2)
+    return slack
 
 
 # -------------------------------------------------------------- RMS norm
@@ -124,6 +134,90 @@ def test_product_at_the_rows_where_its_tile_changes(dtype, experts, fan_out, fan
     y = ns.ns_experts_product_scaled(*x, *w, offsets, numbers, dtype=dtype)
     assert ns.ns_query_last_config().endswith("tile=" + (tile if isinstance(tile, str) else tile[dtype == torch.float32]))
     check_product(y, x, w, offsets, numbers, dtype)
+
+
+# rows, fan_out, fan_in of one matrix: tiles of 32 x 64, of 32 x 32 with k by groups of waves, of 64 x 64, the largest
+ONE_MATRIX = [(10, 64, 272), (10, 64, 528), (200, 4112, 272), (4100, 2832, 656)]
+
+
+def bytes_of(*shape, low, high, seed, dtype):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(low, high, shape, generator=g, dtype=torch.uint8).to(device()).view(dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,fan_out,fan_in", ONE_MATRIX)
+@pytest.mark.parametrize("w_scale", [0, 1, 127, 253, 254])
+def test_product_under_the_least_and_the_largest_scales(dtype, rows, fan_out, fan_in, w_scale):
+    # positive values, so that nothing cancels; x's rows under every kind of scale
+    kinds = torch.tensor([0, 1, 2, 64, 127, 128, 200, 246, 247, 253, 254], dtype=torch.uint8, device=device())
+    x = ns.Scaled(bytes_of(rows, fan_in, low=1, high=127, seed=1, dtype=torch.float8_e4m3fn),
+                  kinds[torch.arange(rows, device=device()) % len(kinds)][:, None].repeat(1, -(-fan_in // 128))
+                  .view(torch.float8_e8m0fnu))
+    w = ns.Scaled(bytes_of(1, fan_out, fan_in, low=1, high=127, seed=2, dtype=torch.float8_e4m3fn),
+                  torch.full((1, -(-fan_out // 128), -(-fan_in // 128)), w_scale, dtype=torch.uint8, device=device())
+                  .view(torch.float8_e8m0fnu))
+    y = ns.ns_experts_product_scaled(*x, w.q[0], w.scales[0], dtype=dtype).double()
+    if dtype == torch.bfloat16:
+        x64, w64 = rows64(x), weights64(w)[0]
+    else:  # the products are those of the values in bf16
+        x64, w64 = ns.ns_dequantize(*x).double(), ns.ns_dequantize(*w)[0].double()
+    want = x64 @ w64.T
+    # a product is off by half a step of fp32 below 2^-126, and so is a result of either type
+    slack = 2 * fan_in * U * want + (fan_in + 1) * 2.0 ** -150 + (2.0 ** -134 if dtype == torch.bfloat16 else 0)
+    if dtype == torch.bfloat16:  # of positive products an eight's largest is at most their sum
+        slack = slack + 2.0 ** -10 * want
+    nan = want.isnan()  # values in bf16 alone: past its largest one, times one that is rounded to zero
+    assert torch.equal(y.isnan(), nan) and not (nan.any() and dtype == torch.bfloat16)
+    fits, passes = want < 2.0 ** 127, want > 2.0 ** 128 * (1 + 2.0 ** -7)
+    assert bool(((y - want).abs() <= HALF[dtype] * want + slack)[fits].all())
+    assert bool((y[passes] == float("inf")).all()) and bool((y[~fits & ~nan] > 2.0 ** 126).all())
+    assert bool(fits.any()) == (dtype == torch.bfloat16 or w_scale < 200)
+
+
+@pytest.mark.parametrize("rows,fan_out,fan_in", ONE_MATRIX)
+def test_product_whose_large_products_cancel(rows, fan_out, fan_in):
+    # eights of 2^9, -2^9 and six of 2^-5: the 8-bit instructions may cut off the six, fp32 results are exact, and they
+    # are what bf16 results of exact products are rounded from
+    a, b = torch.full((rows, fan_in), 2.0 ** -3), torch.full((fan_out, fan_in), 2.0 ** -2)
+    a[:, 0::8], a[:, 1::8] = 2.0 ** 5, -(2.0 ** 5)
+    b[:, 0::8], b[:, 1::8] = 2.0 ** 4, 2.0 ** 4
+    x, w = ns.ns_quantize(a.to(device())), ns.ns_quantize_weights(b.to(device()))
+    assert torch.equal(rows64(x).float(), a.to(device()))
+    want = fan_in / 8 * 6 * 2.0 ** -5
+    assert bool((ns.ns_experts_product_scaled(*x, *w, dtype=torch.float32) == want).all())
+    y = ns.ns_experts_product_scaled(*x, *w).double()
+    assert bool(((y - want).abs() <= HALF[torch.bfloat16] * want + fan_in / 8 * 2.0 ** -10 * 2.0 ** 9).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,fan_in", [(1300, 528), (600, 400), (260, 272)])
+def test_large_tiles_with_absent_rows_and_nan_value_by_value(dtype, tokens, fan_in):
+    # rows that do not exist, experts without rows, rows behind the last expert's, NaN in a row and in a column: every
+    # other value is within its own bound
+    x, w, offsets, rows = large_inputs(tokens, 4, 9, 2064, fan_in, True)
+    n = rows.numel()
+    ends = offsets.clone()
+    ends[3] = ends[2]
+    ends[6:] = n - 37
+    rows = rows.clone()
+    absent = torch.tensor([0, 5, 300, n - 500, n - 38], device=device())
+    rows[absent] = torch.tensor([-1, tokens, 2 ** 31 - 1, -(2 ** 31), tokens + 7], dtype=torch.int32, device=device())
+    x.q.view(torch.uint8)[17, 131] = 0x7f
+    w.q.view(torch.uint8)[1, 1000, 77] = 0xff
+    y = torch.full((n, 2064), 7.0, dtype=dtype, device=device())
+    ns.ns_experts_product_scaled(*x, *w, ends, rows, dtype=dtype, y=y)
+    bad = torch.zeros(n, 2064, dtype=torch.bool, device=device())
+    bad[rows == 17] = True
+    bad[ends[1]:ends[2], 1000] = True
+    bad[n - 37:] = False
+    assert torch.equal(torch.isnan(y), bad) and bool((y[n - 37:] == 7).all())
+    x64, w64, at = rows64(x).nan_to_num(), weights64(w).nan_to_num(), ends.tolist()
+    x64 = torch.where(((rows >= 0) & (rows < tokens))[:, None], x64[rows.clamp(0, tokens - 1).long()], 0.0)
+    for e, (a, b) in enumerate(zip(at, at[1:])):
+        if a < b:
+            off = (y[a:b].double() - x64[a:b] @ w64[e].T).masked_fill(bad[a:b], 0.0).abs()
+            assert bool((off <= bound(x64[a:b], w64[e], dtype)).all()), e
 
 
 # -------------------------------------------------------- weight gradient
