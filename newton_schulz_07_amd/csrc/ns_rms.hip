@@ -9,9 +9,9 @@
 // then see what was normalised.  dx is the gradient of x and of the residual.
 // All of it is bound by HBM; rows are held as layer norm's are (ns_rows.h,
 // rms_shape).  8192 x 7168 bf16: forward with a residual and y in 8 bits 77 us (5.3
-// TB/s of what has to be moved), backward 88 (5.4) and 5 for the sums of dw; a large
-// copy reaches 5.2 TB/s.  A row of 2048: 3.9 us, a launch's latency and a square root
-// in 64 bits.  1003 x 1531 fp32 (rows of odd length): 7.3, 8.4 and 3.9 us, bound by
+// TB/s of what has to be moved), backward 87 (5.4) and 6 for the sums of dw; a large
+// copy reaches 5.2 TB/s.  A row of 2048: 4.0 us, a launch's latency and a square root
+// in 64 bits.  1003 x 1531 fp32 (rows of odd length): 7.4, 8.1 and 3.4 us, bound by
 // latency and the instructions of single-column accesses.
 #include "ns_eight.h"
 #include "ns_rows.h"
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RmsN
 // of the first 512 passes 9 additions (1003 x 1531: dw off by 0.92e-7, root mean square,
 // 1.6e-7 with the runs one after another).  A run's rows are on their way eight at a
 // time, so that 512 rows are one round of loads: latency bounds it (512 rows of 1531
-// columns 3.9 us; 16 runs of 64 columns 5.4).
+// columns 3.4 us; 16 runs of 64 columns 5.4).
 constexpr int kRuns = 64, kRunAhead = 8;
 template <int N> __device__ __forceinline__ float tree_sum(float (&x)[N]) {
 #pragma unroll

@@ -285,9 +285,10 @@ int ns_experts_weight_grad_scaled(const void* dy, const void* x, const uint8_t* 
     if (int s = check_arch()) return s;
     hipStream_t st = static_cast<hipStream_t>(stream);
     // x is restored, then it is the other weight gradient: the k of its products are rows, each with a
-    // scale of its own, which a matrix instruction on 8-bit rows could not apply.  8192 rows of 2048 take
-    // 12 of 510 us (65536 of them named, 128 experts of 1536 x 2048 bf16).  Rows that no one names are
-    // restored too: which are is known on the device only.
+    // scale of its own, which a matrix instruction on 8-bit rows could not apply (a conversion on the way
+    // to the LDS could, 16 bytes of a row having one scale; it is not built).  bf16, 128 experts: 8192
+    // rows of 2048, 65536 times named, take 12 of 512 us; 65536 sorted rows of 1536 49 of 544.  Rows that
+    // no one names are restored too: which are is known on the device only.
     const int64_t used = n_rows == 0 ? 0 : rows != nullptr ? n_x : n_rows;
     const size_t bytes = (size_t)(used * fan_in) * es;
     Workspace ws;  // held to the end of the call's launches
