@@ -255,3 +255,40 @@ def test_weight_gradient_of_a_linear_layer(dtype, n, fan_out, fan_in, gathered):
     assert ns.ns_experts_weight_grad_scaled(dy[:0], x.q[:0], x.scales[:0], dw=out) is out and not out.any()
     with pytest.raises(ValueError):
         ns.ns_experts_weight_grad_scaled(dy, *x, rows=rows, dw=torch.empty(2, fan_out, fan_in, dtype=dtype, device=device()))
+
+
+def test_a_linear_layers_step_captured_poisoned_and_on_another_stream():
+    # norm, product and weight gradient of one matrix, without offsets
+    x, dy = normal(300, 272, seed=1, dtype=torch.bfloat16), normal(300, 144, seed=2, dtype=torch.bfloat16)
+    gamma = 1 + 0.1 * normal(272, seed=3)
+    w, wt = ns.ns_quantize_weights(normal(144, 272, seed=4, scale=272 ** -0.5), transposed=True)
+
+    def step():
+        n = ns.ns_rms_norm(x, gamma, outputs="scaled")
+        y = ns.ns_experts_product_scaled(n.q, n.scales, *w)
+        dw = ns.ns_experts_weight_grad_scaled(dy, n.q, n.scales)
+        dh = ns.ns_experts_product_scaled(*ns.ns_quantize(dy), *wt)
+        return y, dw, *ns.ns_rms_norm_backward(dh, x, gamma, n.rstd)
+
+    def equal(a, b):
+        return all(torch.equal(s, t) for s, t in zip(a, b))
+    first = step()
+    ns.lib().ns_set_workspace_poison(1)
+    try:
+        assert equal(first, step())
+    finally:
+        ns.lib().ns_set_workspace_poison(0)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        assert equal(first, step())  # makes the stream's workspace
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            got = step()
+    torch.cuda.synchronize()
+    for i in range(3):
+        x.copy_(normal(*x.shape, seed=10 + i, dtype=torch.bfloat16))
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert equal(want, got), i
